@@ -40,6 +40,10 @@ EXPORTED = [
     "ttt_selftest_gemm", "ttt_profile_enable", "ttt_profile_collect", "ttt_stage_name", "ttt_launch_count",
     "ttt_forward_noalloc", "ttt_token_pair_capacity", "ttt_selftest_timeout", "ttt_plan_info",
     "ttt_state_size", "ttt_forward_state", "ttt_selftest_activation", "ttt_pair_schedule",
+    "ttt_rope_create", "ttt_rope_destroy", "ttt_rope_apply",
+    "ttt_scan_create", "ttt_scan_destroy", "ttt_scan_workspace_size", "ttt_scan_saved_size", "ttt_scan_forward",
+    "ttt_scan_backward",
+    "ttt_norm_create", "ttt_norm_destroy", "ttt_norm_workspace_size", "ttt_norm_forward", "ttt_norm_backward",
 ]
 NUM_STAGES = 8
 
@@ -92,6 +96,22 @@ def _load():
         "ttt_plan_info": (i32, [vp, ctypes.POINTER(ctypes.c_int), i32]),
         "ttt_state_size": (sz, [vp]),
         "ttt_forward_state": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        # the operators of ttt_ops.h (strides are passed as pointers to three int64)
+        "ttt_rope_create": (i32, [vp, ctypes.POINTER(vp)]),
+        "ttt_rope_destroy": (None, [vp]),
+        "ttt_rope_apply": (i32, [vp, i32, i32, i64, vp, vp, vp, i32, i64, vp, vp, i32, vp]),
+        "ttt_scan_create": (i32, [vp, ctypes.POINTER(vp)]),
+        "ttt_scan_destroy": (None, [vp]),
+        "ttt_scan_workspace_size": (sz, [vp, i32, i64]),
+        "ttt_scan_saved_size": (sz, [vp, i32, i64]),
+        "ttt_scan_forward": (i32, [vp, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]),
+        "ttt_scan_backward": (i32, [vp, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp,
+                                    vp]),
+        "ttt_norm_create": (i32, [vp, ctypes.POINTER(vp)]),
+        "ttt_norm_destroy": (None, [vp]),
+        "ttt_norm_workspace_size": (sz, [vp, i32, i64, i32]),
+        "ttt_norm_forward": (i32, [vp, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]),
+        "ttt_norm_backward": (i32, [vp, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
