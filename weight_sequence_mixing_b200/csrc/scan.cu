@@ -2,15 +2,57 @@
 //   h_t = a_t h_{t-1} + u_t,   a = g | sigma(g) | exp(g),   u = x | (1 - a) x.
 // Backward: lam_t = dh_t + mu_t with mu_t = a_{t+1} lam_{t+1}, the gradient that
 // reaches h_t from the later tokens (mu_len = dh_last).
+//
+// A step is an affine map of the state, and maps compose: a run of tokens takes a
+// state s to A s + H with A the product of its gates and H its result from zero.  So
+// the tokens are cut into tiles.  A tile's (A, H) needs only its own rows; the state that
+// enters it comes from the tiles before: each tile publishes its (A, H), finds the nearest
+// earlier tile whose outgoing state is known, applies the maps in between in token order,
+// and publishes its own outgoing state.  Every input is read once and every output
+// written once: the bound is HBM.
+//   - A block's warps have three trades.  One fetches the rows of the tiles to come into
+//     a ring of stages (TMA; rows that TMA cannot address, on strides that are no multiple
+//     of 16 bytes, by 4-byte asynchronous copies or plain loads).  Eight sweep a tile's
+//     rows twice: first for the maps, and one tile later, when the states that enter are
+//     there, for the states themselves.  One follows the chain of states from tile to tile.
+//     So a tile's state is waited for while the next tile's maps are formed, and loads run
+//     on throughout.  The gates are formed in both sweeps: keeping them (8 bytes a value
+//     in registers) was measured, and it holds too few tokens in flight for the chain's
+//     latency (scene layer of 1029120 tokens, 1024 channels: 5.98 ms, against FWD_MS here).
+//   - A warp takes the same channels of a few consecutive tokens; a lane one 4-byte word
+//     of channels of each.
+//   - Tiles are handed out by a counter, tokens first to last, so a tile only waits for
+//     tiles of blocks that already run: the order of the hardware's blocks does not matter,
+//     nor what else runs on the GPU.
+//   - The state that enters a tile is always a known state with the maps applied one by
+//     one, so a result has the same bits whichever tile's state was found first.
+// The backward pass is the same over the tokens last to first; the states h_{t-1} that the
+// gates' gradient needs are formed again in fp32 from states that the forward pass kept
+// (one in 64 tokens), not read back rounded.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <new>
 
 #include "op_checks.h"
+#include "per_device.h"
+#include "ptx.cuh"
+#include "tc_gemm.cuh"
+#include "ttt_plan.cuh"
 
 namespace ttt {
 namespace {
+
+constexpr int kWarps = 8;          // warps that sweep a tile's rows
+constexpr int kChainWarp = 8;      // the warp that follows the chain of states
+constexpr int kFeedWarp = 9;       // the warp that fetches rows
+constexpr int kThreads = 32 * 10;
+constexpr int kRowBytes = 128;     // a tile's channels: 32 lanes of 4 bytes
+constexpr int kSave = 64;          // tokens from one kept state to the next
+constexpr int kShort = 16;         // longest sequence of the short form
+constexpr int kWindow = 64;        // earlier tiles looked at
+enum : int { kLoadTma = 0, kLoad4 = 1, kLoad2 = 2 };
 
 struct ScanArgs {
   const void *g, *x, *dh;
@@ -21,33 +63,132 @@ struct ScanArgs {
   int64_t gs[2], xs[2], hs[2], dhs[2], dgs[2], dxs[2];  // batch, token
   int64_t L;
   int32_t B, D;
+  // tiles
+  unsigned* counter;  // next tile to hand out; null: by block index, one tile a sequence
+  uint64_t* maps;     // [tile][channel of the tile] (A, H)
+  uint32_t* states;   // [tile][channel of the tile]
+  unsigned* status;
+  int32_t cols, per_col;  // columns of channels; tiles of a sequence
+  int32_t total;          // tiles in all
+  int32_t load;           // kLoadTma, kLoad4, kLoad2
+  int32_t wide;           // outputs take 4-byte stores
+  int32_t kept;           // kept states of a sequence
 };
 
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+// The values of a lane's 4 bytes: one fp32 or two bf16, these in the packed fp32
+// arithmetic of sm_100 (one instruction for both).
+struct One {
+  float v;
+  __device__ __forceinline__ float operator[](int) const { return v; }
+};
+struct Two {
+  uint64_t w;
+  __device__ __forceinline__ float operator[](int i) const { return __uint_as_float(uint32_t(i ? w >> 32 : w)); }
+};
+__device__ __forceinline__ Two two(float a, float b) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.w) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ One fma_(One a, One b, One c) { return {fmaf(a.v, b.v, c.v)}; }
+__device__ __forceinline__ One mul_(One a, One b) { return {a.v * b.v}; }
+__device__ __forceinline__ One add_(One a, One b) { return {a.v + b.v}; }
+__device__ __forceinline__ One sub_(One a, One b) { return {a.v - b.v}; }
+__device__ __forceinline__ Two fma_(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.w) : "l"(a.w), "l"(b.w), "l"(c.w));
+  return r;
+}
+__device__ __forceinline__ Two mul_(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.w) : "l"(a.w), "l"(b.w));
+  return r;
+}
+__device__ __forceinline__ Two add_(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.w) : "l"(a.w), "l"(b.w));
+  return r;
+}
+__device__ __forceinline__ Two sub_(Two a, Two b) { return fma_(b, two(-1.f, -1.f), a); }
 
-// a and 1 - a; the complement is formed on its own, so that it keeps its digits
-// where a is close to 1
-template <int GATE>
-__device__ __forceinline__ void gate(float g, float& a, float& rest) {
-  if (GATE == TTT_GATE_VALUE) {
+template <class T>
+struct Word;
+template <>
+struct Word<float> {
+  static constexpr int N = 1;
+  using V = One;
+  static __device__ __forceinline__ V all(float v) { return {v}; }
+  static __device__ __forceinline__ V make(const float (&v)[1]) { return {v[0]}; }
+  static __device__ __forceinline__ V open(uint32_t w) { return {__uint_as_float(w)}; }
+  static __device__ __forceinline__ uint32_t close(V v) { return __float_as_uint(v.v); }
+};
+template <>
+struct Word<__nv_bfloat16> {
+  static constexpr int N = 2;
+  using V = Two;
+  static __device__ __forceinline__ V all(float v) { return two(v, v); }
+  static __device__ __forceinline__ V make(const float (&v)[2]) { return two(v[0], v[1]); }
+  static __device__ __forceinline__ V open(uint32_t w) {
+    return two(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint32_t close(V v) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(v[0], v[1]);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  }
+};
+
+__device__ __forceinline__ float exp2_fast(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// a and 1 - a of a lane's values; the complement is formed on its own, so that it keeps
+// its digits where a is close to 1.  bf16 inputs take the hardware's exponential and
+// reciprocal (a few units of 2^-24 off), fp32 ones the library's.
+template <class T, int GATE>
+__device__ __forceinline__ void gate(typename Word<T>::V g, typename Word<T>::V& a, typename Word<T>::V& rest) {
+  using W = Word<T>;
+  if constexpr (GATE == TTT_GATE_VALUE) {
     a = g;
-    rest = 1.f - g;
-  } else if (GATE == TTT_GATE_SIGMOID) {
-    a = 1.f / (1.f + expf(-g));
-    rest = 1.f / (1.f + expf(g));
+    rest = sub_(W::all(1.f), g);
+  } else if constexpr (sizeof(T) == 2) {
+    const Two y = mul_(g, W::all(GATE == TTT_GATE_SIGMOID ? -1.4426950408889634f : 1.4426950408889634f));
+    const Two e = two(exp2_fast(y[0]), exp2_fast(y[1]));
+    if constexpr (GATE == TTT_GATE_SIGMOID) {
+      const Two s = add_(e, W::all(1.f));
+      a = two(rcp_fast(s[0]), rcp_fast(s[1]));
+      const Two q = mul_(e, a);  // infinity times zero where the gate is shut: the complement is one
+      rest = two(fminf(q[0], 1.f), fminf(q[1], 1.f));
+    } else {
+      a = e;
+      rest = two(-expm1f(g[0]), -expm1f(g[1]));
+    }
+  } else if constexpr (GATE == TTT_GATE_SIGMOID) {  // of e^-|g| in (0, 1]: nothing overflows
+    const float e = expf(-fabsf(g.v));
+    const float p = 1.f / (1.f + e), q = e * p;
+    a.v = g.v < 0.f ? q : p;
+    rest.v = g.v < 0.f ? p : q;
   } else {
-    a = expf(g);
-    rest = -expm1f(g);
+    a.v = expf(g.v);
+    rest.v = -expm1f(g.v);
   }
 }
 // d gate / d g times `v`
-template <int GATE>
-__device__ __forceinline__ float gate_grad(float a, float rest, float v) {
-  return GATE == TTT_GATE_VALUE ? v : GATE == TTT_GATE_EXP ? v * a : v * a * rest;
+template <int GATE, class V>
+__device__ __forceinline__ V gate_grad(V a, V rest, V v) {
+  if constexpr (GATE == TTT_GATE_VALUE) return v;
+  else if constexpr (GATE == TTT_GATE_EXP) return mul_(v, a);
+  else return mul_(mul_(v, a), rest);
 }
+
+// A s + H.  A state of zero gives H even where the product of the gates overflowed.
+__device__ __forceinline__ float apply(float A, float H, float s) { return s == 0.f ? H : fmaf(A, s, H); }
 
 __device__ __forceinline__ int64_t length_of(const ScanArgs& p, int b) {
   if (!p.lengths) return p.L;
@@ -55,67 +196,595 @@ __device__ __forceinline__ int64_t length_of(const ScanArgs& p, int b) {
   return n < 0 ? 0 : n > p.L ? p.L : n;
 }
 
-// One thread per (batch entry, channel), token after token.  saved: h_{t-1} of every
-// token, fp32.
-template <class T, int GATE, int INPUT>
-__global__ void scan_forward_kernel(const __grid_constant__ ScanArgs p) {
-  const int64_t k = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (k >= int64_t(p.B) * p.D) return;
-  const int b = int(k / p.D), c = int(k % p.D);
-  const int64_t len = length_of(p, b);
-  const T* g = static_cast<const T*>(p.g) + b * p.gs[0] + c;
-  const T* x = static_cast<const T*>(p.x) + b * p.xs[0] + c;
-  T* h = static_cast<T*>(p.h) + b * p.hs[0] + c;
-  float s = p.h0 ? p.h0[k] : 0.f;
-  for (int64_t t = 0; t < len; ++t) {
-    float a, rest;
-    gate<GATE>(to_f(g[t * p.gs[1]]), a, rest);
-    const float v = to_f(x[t * p.xs[1]]);
-    if (p.saved) p.saved[(int64_t(b) * p.L + t) * p.D + c] = s;
-    s = a * s + (INPUT == TTT_SCAN_COMPLEMENT ? rest * v : v);
-    put(h + t * p.hs[1], s);
-  }
-  if (p.h_last) p.h_last[k] = s;
+struct Place {
+  int b, col, i;  // batch entry, column of channels, tile of the sequence in token order
+};
+template <bool BACKWARD>
+__device__ __forceinline__ Place place_of(const ScanArgs& p, int t) {
+  const int columns = p.B * p.cols;  // fits: one tile a column at least
+  const int k = t / columns, r = t - k * columns;
+  return {r / p.cols, r % p.cols, BACKWARD ? p.per_col - 1 - k : k};
 }
 
-template <class T, int GATE, int INPUT>
-__global__ void scan_backward_kernel(const __grid_constant__ ScanArgs p) {
-  const int64_t k = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (k >= int64_t(p.B) * p.D) return;
-  const int b = int(k / p.D), c = int(k % p.D);
-  const int64_t len = length_of(p, b);
-  const T* g = static_cast<const T*>(p.g) + b * p.gs[0] + c;
-  const T* x = static_cast<const T*>(p.x) + b * p.xs[0] + c;
-  const T* dh = static_cast<const T*>(p.dh) + b * p.dhs[0] + c;
-  T* dg = static_cast<T*>(p.dg) + b * p.dgs[0] + c;
-  T* dx = static_cast<T*>(p.dx) + b * p.dxs[0] + c;
-  float mu = p.dh_last ? p.dh_last[k] : 0.f;
-  for (int64_t t = len - 1; t >= 0; --t) {
-    float a, rest;
-    gate<GATE>(to_f(g[t * p.gs[1]]), a, rest);
-    const float lam = to_f(dh[t * p.dhs[1]]) + mu;
-    float d = p.saved[(int64_t(b) * p.L + t) * p.D + c];
-    if (INPUT == TTT_SCAN_COMPLEMENT) d -= to_f(x[t * p.xs[1]]);
-    put(dx + t * p.dxs[1], INPUT == TTT_SCAN_COMPLEMENT ? rest * lam : lam);
-    put(dg + t * p.dgs[1], gate_grad<GATE>(a, rest, lam * d));
-    mu = a * lam;
-  }
-  if (p.dh0) p.dh0[k] = mu;
+// Published maps and states carry their own readiness: the memory starts as all ones (a
+// NaN that no value is stored as), and a map is one 8-byte word, so a reader needs no
+// flag and a writer no fence.
+constexpr uint32_t kAbsent = 0xffffffffu;
+__device__ __forceinline__ uint32_t present(float v) {
+  const uint32_t w = __float_as_uint(v);
+  return w == kAbsent ? 0x7fffffffu : w;
+}
+template <int N>
+__device__ __forceinline__ void publish_map(const ScanArgs& p, int t, const float (&A)[N], const float (&H)[N]) {
+  uint64_t w[N];
+#pragma unroll
+  for (int v = 0; v < N; ++v) w[v] = uint64_t(present(H[v])) << 32 | present(A[v]);
+  uint64_t* to = p.maps + (int64_t(t) * 32 + threadIdx.x % 32) * N;
+  if constexpr (N == 2)
+    asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};" ::"l"(to), "l"(w[0]), "l"(w[N - 1]) : "memory");
+  else
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(to), "l"(w[0]) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void publish_state(const ScanArgs& p, int t, const float (&s)[N]) {
+  uint32_t* to = p.states + (int64_t(t) * 32 + threadIdx.x % 32) * N;
+  if constexpr (N == 2)
+    asm volatile("st.relaxed.gpu.global.v2.u32 [%0], {%1, %2};" ::"l"(to), "r"(present(s[0])), "r"(present(s[N - 1]))
+                 : "memory");
+  else
+    asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(to), "r"(present(s[0])) : "memory");
+}
+// This lane's words of a tile, and whether a word is there
+template <int N>
+__device__ __forceinline__ void load_map(const ScanArgs& p, int t, uint64_t (&w)[N]) {
+  const uint64_t* from = p.maps + (int64_t(t) * 32 + threadIdx.x % 32) * N;
+  if constexpr (N == 2)
+    asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];" : "=l"(w[0]), "=l"(w[N - 1]) : "l"(from));
+  else
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(w[0]) : "l"(from));
+}
+template <int N>
+__device__ __forceinline__ void load_state(const ScanArgs& p, int t, uint32_t (&w)[N]) {
+  const uint32_t* from = p.states + (int64_t(t) * 32 + threadIdx.x % 32) * N;
+  if constexpr (N == 2)
+    asm volatile("ld.relaxed.gpu.global.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[N - 1]) : "l"(from));
+  else
+    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(w[0]) : "l"(from));
+}
+__device__ __forceinline__ float apply_word(uint64_t w, float s) {
+  return apply(__uint_as_float(uint32_t(w)), __uint_as_float(uint32_t(w >> 32)), s);
 }
 
-using ScanKernel = void (*)(const ScanArgs);
+// The state that enters tile `t` (the chain warp; `before` earlier tiles of its
+// column, `step` tiles apart): see the top of the file.  Looks at kNear tiles at a time, nearest first, and
+// farther as long as all nearer maps are there.  A wait that runs out gives NaN.
+constexpr int kNear = 8;
+template <int N>
+__device__ __forceinline__ void look_back(const ScanArgs& p, int t, int before, int step, float (&s)[N]) {
+  unsigned long long since = 0;
+  for (int spin = 0;; ++spin) {
+    for (int d = 0; d < kWindow && d < before; d += kNear) {  // tiles d + 1 .. d + kNear back
+      uint64_t map[kNear][N];
+      uint32_t st[kNear][N];
+      // all loads first, so that one trip to L2 brings the window (past the first tile: the first again)
+#pragma unroll
+      for (int e = 0; e < kNear; ++e) {
+        const int q = t - min(d + e + 1, before) * step;
+        load_state<N>(p, q, st[e]);
+        load_map<N>(p, q, map[e]);
+      }
+      unsigned maps = 0, states = 0;
+#pragma unroll
+      for (int e = 0; e < kNear; ++e) {
+        const bool in = d + e < before;
+        maps |= unsigned(in && uint32_t(map[e][0]) != kAbsent && uint32_t(map[e][N - 1]) != kAbsent) << e;
+        states |= unsigned(in && st[e][0] != kAbsent && st[e][N - 1] != kAbsent) << e;
+      }
+      maps = __reduce_and_sync(~0u, maps);
+      states = __reduce_and_sync(~0u, states);
+      if (states) {
+        const int j = __ffs(states) - 1;
+        if ((~maps & ((1u << j) - 1)) == 0) {
+#pragma unroll
+          for (int e = kNear - 1; e >= 0; --e) {
+#pragma unroll
+            for (int v = 0; v < N; ++v) {
+              if (e == j) s[v] = __uint_as_float(st[e][v]);
+              if (e < j) s[v] = apply_word(map[e][v], s[v]);
+            }
+          }
+          for (int q = d; q > 0; q -= kNear) {  // the windows before this one are all there
+#pragma unroll
+            for (int e = 0; e < kNear; ++e) load_map<N>(p, t - (q - e) * step, map[e]);
+#pragma unroll
+            for (int e = 0; e < kNear; ++e)
+#pragma unroll
+              for (int v = 0; v < N; ++v) s[v] = apply_word(map[e][v], s[v]);
+          }
+          return;
+        }
+        break;
+      }
+      if (maps != (1u << kNear) - 1) break;
+    }
+    if (spin % 64 == 63) {
+      const unsigned long long now = __shfl_sync(~0u, global_ns(), 0);
+      if (!since) since = now;
+      if (now - since > kWaitLimitNs) break;
+    }
+  }
+  if (threadIdx.x % 32 == 0 && p.status) atomicOr(p.status, kStatusTimeout);
+#pragma unroll
+  for (int v = 0; v < N; ++v) s[v] = __int_as_float(0x7fc00000);
+}
+
+// A row's word of one output
 template <class T>
-ScanKernel pick(bool backward, int gate, int input) {
-#define TTT_SCAN_PICK(G, I) \
-  if (gate == G && input == I) return backward ? scan_backward_kernel<T, G, I> : scan_forward_kernel<T, G, I>;
-  TTT_SCAN_PICK(TTT_GATE_VALUE, TTT_SCAN_PLAIN)
-  TTT_SCAN_PICK(TTT_GATE_VALUE, TTT_SCAN_COMPLEMENT)
-  TTT_SCAN_PICK(TTT_GATE_SIGMOID, TTT_SCAN_PLAIN)
-  TTT_SCAN_PICK(TTT_GATE_SIGMOID, TTT_SCAN_COMPLEMENT)
-  TTT_SCAN_PICK(TTT_GATE_EXP, TTT_SCAN_PLAIN)
-  TTT_SCAN_PICK(TTT_GATE_EXP, TTT_SCAN_COMPLEMENT)
-#undef TTT_SCAN_PICK
-  return nullptr;
+__device__ __forceinline__ void put_word(const ScanArgs& p, T* to, int c, typename Word<T>::V v) {
+  const uint32_t w = Word<T>::close(v);
+  if (Word<T>::N == 1 || p.wide) {
+    *reinterpret_cast<uint32_t*>(to) = w;
+  } else {
+    uint16_t* h = reinterpret_cast<uint16_t*>(to);
+    h[0] = uint16_t(w);
+    if (c + 1 < p.D) h[1] = uint16_t(w >> 16);
+  }
+}
+
+// Tiles of 128 tokens forward and 64 backward (one tensor more), three and four stages:
+// 96 KB, two blocks an SM.
+template <class T, bool BACKWARD>
+struct Shape {
+  static constexpr int N = Word<T>::N;
+  static constexpr int kRows = BACKWARD ? 8 : 16;  // tokens of a warp
+  static constexpr int kTile = kWarps * kRows;
+  static constexpr int kBox = kTile * kRowBytes;  // bytes of one tensor's tile
+  static constexpr int kTensors = BACKWARD ? 3 : 2;
+  static constexpr int kStages = 3;
+  static constexpr int kStageBytes = kTensors * kBox;
+  struct Scratch {  // behind the stages; two of each by parity of the block's tiles
+    float A[2][kWarps][32 * N], H[2][kWarps][32 * N];  // each warp's map
+    float R[BACKWARD ? 2 : 1][BACKWARD ? kWarps : 1][32 * N];   // backward: its map's (A, R) of mu
+    float in[2][kWarps][32 * N];                                // the state that enters each warp's rows
+    float back[BACKWARD ? 2 : 1][BACKWARD ? kWarps : 1][32 * N];  // backward: the mu that enters
+    uint64_t full[kStages], empty[kStages];  // a stage's rows are there; are done with
+    uint64_t mapped[2], entered[2];          // a tile's maps are there; its states
+    int tile[kStages];                       // the stages' tiles, or -1: no more
+    int abort;
+  };
+  static constexpr int kSmem = 1024 + kStages * kStageBytes + int(sizeof(Scratch));
+};
+
+// One tensor's rows of a tile into shared memory, at the swizzle TMA uses, by one warp
+template <class T, int TILE>
+__device__ __forceinline__ void fetch(const ScanArgs& p, const void* base, const int64_t (&s)[2], int b, int c, int64_t t0,
+                                      int64_t len, uint8_t* dst) {
+  const int lane = threadIdx.x % 32;
+  const T* src = static_cast<const T*>(base) + b * s[0] + c;
+#pragma unroll 8
+  for (int r = 0; r < TILE; ++r) {
+    uint32_t* to = reinterpret_cast<uint32_t*>(dst + r * kRowBytes + ((lane * 4) ^ ((r & 7) << 4)));
+    const bool live = t0 + r < len && c < p.D;
+    const T* from = live ? src + (t0 + r) * s[1] : static_cast<const T*>(base);
+    if (p.load == kLoad4) {  // nothing is read where the size is 0: zero-filled
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(live ? 4 : 0)
+                   : "memory");
+    } else {
+      uint32_t w = 0;
+      if (live) {
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(from);
+        w = h[0];
+        if (Word<T>::N == 2 && c + 1 < p.D) w |= uint32_t(h[1]) << 16;
+      }
+      *to = w;
+    }
+  }
+}
+
+template <class T, int GATE, int INPUT, bool BACKWARD>
+__global__ void __launch_bounds__(kThreads, 2)
+    scan_tile_kernel(const __grid_constant__ ScanArgs p, const __grid_constant__ CUtensorMap mg,
+                     const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap md) {
+  using S = Shape<T, BACKWARD>;
+  using W = Word<T>;
+  using V = typename W::V;
+  constexpr int N = S::N, kStages = S::kStages, kTile = S::kTile, kRows = S::kRows;
+  extern __shared__ uint8_t raw[];
+  uint8_t* const stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  typename S::Scratch& sc = *reinterpret_cast<typename S::Scratch*>(stages + kStages * S::kStageBytes);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int step = p.B * p.cols;  // tiles from one of a column to its next
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sc.full[s], p.load == kLoadTma ? 1 : 32);
+      mbar_init(&sc.empty[s], kWarps);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sc.mapped[s], kWarps);
+      mbar_init(&sc.entered[s], 1);
+    }
+    fence_mbar_init();
+    sc.abort = 0;
+  }
+  __syncthreads();
+
+  // Every wait is bounded; one that runs out ends the block's work with the status set.
+  auto wait = [&](uint64_t* bar, int turn) {
+    const bool ok = mbar_wait(bar, turn & 1, &sc.abort);
+    if (!ok && p.status && lane == 0) atomicOr(p.status, kStatusTimeout);
+    return __all_sync(~0u, ok) != 0;
+  };
+
+  if (warp == kFeedWarp) {
+    int k = 0, turn = 0;
+    for (bool more = true; more; ++turn) {
+      int t = 0;
+      if (lane == 0) t = p.counter ? int(atomicAdd(p.counter, 1u) + 1u) : int(blockIdx.x) + turn * int(gridDim.x);
+      t = __shfl_sync(~0u, t, 0);
+      more = t < p.total;
+      Place at{};
+      int64_t len = 0, t0 = 0;
+      if (more) {
+        at = place_of<BACKWARD>(p, t);
+        len = length_of(p, at.b);
+        t0 = int64_t(at.i) * kTile;
+        if (t0 >= len) {
+          if (len == 0 && at.i == 0)  // an empty sequence hands its state through
+            for (int v = 0; v < N; ++v) {
+              const int c = (at.col * 32 + lane) * N + v;
+              if (c >= p.D) continue;
+              const int64_t e = int64_t(at.b) * p.D + c;
+              const float* from = BACKWARD ? p.dh_last : p.h0;
+              float* to = BACKWARD ? p.dh0 : p.h_last;
+              if (to) to[e] = from ? from[e] : 0.f;
+            }
+          continue;
+        }
+      }
+      const int s = k % kStages;
+      if (k >= kStages && !wait(&sc.empty[s], k / kStages - 1)) break;
+      if (lane == 0) sc.tile[s] = more ? t : -1;
+      __syncwarp();
+      uint8_t* const to = stages + s * S::kStageBytes;
+      const int c0 = at.col * 32 * N;
+      if (p.load == kLoadTma) {
+        if (lane == 0) {
+          if (more) {
+            mbar_arrive_expect_tx(&sc.full[s], S::kStageBytes);
+            tma_load_3d(to, &mg, &sc.full[s], c0, int(t0), at.b);
+            tma_load_3d(to + S::kBox, &mx, &sc.full[s], c0, int(t0), at.b);
+            if (BACKWARD) tma_load_3d(to + 2 * S::kBox, &md, &sc.full[s], c0, int(t0), at.b);
+          } else {
+            mbar_arrive(&sc.full[s]);
+          }
+        }
+      } else {
+        if (more) {
+          fetch<T, kTile>(p, p.g, p.gs, at.b, c0 + lane * N, t0, len, to);
+          fetch<T, kTile>(p, p.x, p.xs, at.b, c0 + lane * N, t0, len, to + S::kBox);
+          if (BACKWARD) fetch<T, kTile>(p, p.dh, p.dhs, at.b, c0 + lane * N, t0, len, to + 2 * S::kBox);
+        }
+        if (p.load == kLoad4)  // arrives when this lane's copies have
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sc.full[s])) : "memory");
+        else
+          mbar_arrive(&sc.full[s]);
+      }
+      ++k;
+    }
+    // copies in flight end before the block does: after a wait that ran out, nobody else waits for them
+    if (*(volatile int*)&sc.abort) {
+      int given_up = 0;
+      for (int m = k > kStages ? k - kStages : 0; m < k; ++m) mbar_wait(&sc.full[m % kStages], m / kStages & 1, &given_up);
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+    return;
+  }
+
+  if (warp == kChainWarp) {
+    for (int k = 0;; ++k) {
+      const int s = k % kStages, par = k & 1;
+      if (!wait(&sc.full[s], k / kStages)) return;
+      const int t = *(volatile int*)&sc.tile[s];
+      if (t < 0) return;
+      const Place at = place_of<BACKWARD>(p, t);
+      const int64_t len = length_of(p, at.b);
+      const int last = int((len - 1) / kTile);
+      const int before = BACKWARD ? last - at.i : at.i;
+      const bool wanted = BACKWARD ? at.i > 0 : at.i < last;  // another tile needs this one's state
+      const int c = (at.col * 32 + lane) * N;
+      const int64_t e = int64_t(at.b) * p.D + c;
+      float A[N], H[N], st[N];
+#pragma unroll
+      for (int v = 0; v < N; ++v) {
+        const float* from = BACKWARD ? p.dh_last : p.h0;
+        st[v] = before == 0 && from && c + v < p.D ? from[e + v] : 0.f;
+      }
+      if (BACKWARD) {
+        // the states h that enter the warps' rows, from the kept one that entered the tile
+        float h[N];
+#pragma unroll
+        for (int v = 0; v < N; ++v)
+          h[v] = c + v < p.D ? __ldg(p.saved + (int64_t(at.b) * p.kept + at.i * (kTile / kSave)) * p.D + c + v) : 0.f;
+        if (!wait(&sc.mapped[par], k / 2)) return;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+          for (int v = 0; v < N; ++v) {
+            sc.in[par][w][lane * N + v] = h[v];
+            h[v] = apply(sc.A[par][w][lane * N + v], sc.H[par][w][lane * N + v], h[v]);
+          }
+      } else if (!wait(&sc.mapped[par], k / 2)) {
+        return;
+      }
+      float wa[kWarps][N], wh[kWarps][N];  // the warps' maps, in the order of the chain
+#pragma unroll
+      for (int j = 0; j < kWarps; ++j)
+#pragma unroll
+        for (int v = 0; v < N; ++v) {
+          const int w = BACKWARD ? kWarps - 1 - j : j;
+          wa[j][v] = sc.A[par][w][lane * N + v];
+          wh[j][v] = BACKWARD ? sc.R[par][w][lane * N + v] : sc.H[par][w][lane * N + v];
+        }
+#pragma unroll
+      for (int v = 0; v < N; ++v) {
+        A[v] = 1.f, H[v] = 0.f;
+#pragma unroll
+        for (int j = 0; j < kWarps; ++j) {
+          H[v] = apply(wa[j][v], wh[j][v], H[v]);
+          A[v] *= wa[j][v];
+        }
+      }
+      if (before > 0) {
+        if (wanted) publish_map<N>(p, t, A, H);
+        look_back<N>(p, t, before, step, st);
+      }
+      float out[N];
+#pragma unroll
+      for (int v = 0; v < N; ++v) out[v] = apply(A[v], H[v], st[v]);
+      if (wanted) publish_state<N>(p, t, out);
+#pragma unroll
+      for (int j = 0; j < kWarps; ++j) {
+        const int w = BACKWARD ? kWarps - 1 - j : j;
+#pragma unroll
+        for (int v = 0; v < N; ++v) {
+          if (BACKWARD)
+            sc.back[par][w][lane * N + v] = st[v];
+          else
+            sc.in[par][w][lane * N + v] = st[v];
+          if (!BACKWARD && w * kRows % kSave == 0 && p.saved && c + v < p.D &&
+              int64_t(at.i) * kTile + w * kRows < len)
+            p.saved[(int64_t(at.b) * p.kept + at.i * (kTile / kSave) + w * kRows / kSave) * p.D + c + v] = st[v];
+          st[v] = apply(wa[j][v], wh[j][v], st[v]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sc.entered[par]);
+#pragma unroll
+      for (int v = 0; v < N; ++v)
+        if (c + v < p.D) {
+          if (BACKWARD) {
+            if (at.i == 0 && p.dh0) p.dh0[e + v] = out[v];
+          } else if (at.i == last && p.h_last) {
+            p.h_last[e + v] = out[v];
+          }
+        }
+    }
+  }
+
+  // the sweeping warps: the maps of tile k + 1, then the states of tile k
+  int cur = -1;
+  for (int k = -1;; ++k) {
+    int next = -1;
+    if (k < 0 || cur >= 0) {
+      const int s = (k + 1) % kStages, par = (k + 1) & 1;
+      if (!wait(&sc.full[s], (k + 1) / kStages)) return;
+      next = *(volatile int*)&sc.tile[s];
+      if (next >= 0) {
+        const Place at = place_of<BACKWARD>(p, next);
+        const int64_t left = length_of(p, at.b) - (int64_t(at.i) * kTile + warp * kRows);
+        const uint8_t* const rows = stages + s * S::kStageBytes + warp * kRows * kRowBytes;
+        V A = W::all(1.f), H = W::all(0.f), R = W::all(0.f);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          const int at4 = r * kRowBytes + ((lane * 4) ^ ((r & 7) << 4));
+          const V g = W::open(*reinterpret_cast<const uint32_t*>(rows + at4));
+          const V x = W::open(*reinterpret_cast<const uint32_t*>(rows + S::kBox + at4));
+          if (r < left) {  // rows behind the end hold anything
+            V a, rest;
+            gate<T, GATE>(g, a, rest);
+            H = fma_(a, H, INPUT == TTT_SCAN_COMPLEMENT ? mul_(rest, x) : x);
+            A = mul_(A, a);
+            if (BACKWARD)
+              R = fma_(A, W::open(*reinterpret_cast<const uint32_t*>(rows + 2 * S::kBox + at4)), R);
+          }
+        }
+#pragma unroll
+        for (int v = 0; v < N; ++v) {
+          sc.A[par][warp][lane * N + v] = A[v];
+          sc.H[par][warp][lane * N + v] = H[v];
+          if (BACKWARD) sc.R[par][warp][lane * N + v] = R[v];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sc.mapped[par]);
+      }
+    }
+    if (k >= 0) {
+      if (cur < 0) return;
+      const int s = k % kStages, par = k & 1;
+      const Place at = place_of<BACKWARD>(p, cur);
+      const int64_t t0 = int64_t(at.i) * kTile + warp * kRows;
+      const int64_t left = length_of(p, at.b) - t0;
+      const int c = (at.col * 32 + lane) * N;
+      const uint8_t* const rows = stages + s * S::kStageBytes + warp * kRows * kRowBytes;
+      if (!wait(&sc.entered[par], k / 2)) return;
+      float in[N];
+#pragma unroll
+      for (int v = 0; v < N; ++v) in[v] = sc.in[par][warp][lane * N + v];
+      V st = W::make(in);
+      if constexpr (!BACKWARD) {
+        T* to = static_cast<T*>(p.h) + at.b * p.hs[0] + t0 * p.hs[1] + c;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r, to += p.hs[1]) {
+          const int at4 = r * kRowBytes + ((lane * 4) ^ ((r & 7) << 4));
+          const V g = W::open(*reinterpret_cast<const uint32_t*>(rows + at4));
+          const V x = W::open(*reinterpret_cast<const uint32_t*>(rows + S::kBox + at4));
+          V a, rest;
+          gate<T, GATE>(g, a, rest);
+          st = fma_(a, st, INPUT == TTT_SCAN_COMPLEMENT ? mul_(rest, x) : x);
+          if (r < left && c < p.D) put_word<T>(p, to, c, st);
+        }
+      } else {
+        // h_{t-1} (less x_t) of the rows first to last, then the gradients last to first
+        V a[kRows], rest[kRows], d[kRows];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          const int at4 = r * kRowBytes + ((lane * 4) ^ ((r & 7) << 4));
+          const V g = W::open(*reinterpret_cast<const uint32_t*>(rows + at4));
+          const V x = W::open(*reinterpret_cast<const uint32_t*>(rows + S::kBox + at4));
+          gate<T, GATE>(g, a[r], rest[r]);
+          d[r] = INPUT == TTT_SCAN_COMPLEMENT ? sub_(st, x) : st;
+          st = fma_(a[r], st, INPUT == TTT_SCAN_COMPLEMENT ? mul_(rest[r], x) : x);
+        }
+#pragma unroll
+        for (int v = 0; v < N; ++v) in[v] = sc.back[par][warp][lane * N + v];
+        V mu = W::make(in);
+        T* dx = static_cast<T*>(p.dx) + at.b * p.dxs[0] + (t0 + kRows) * p.dxs[1] + c;
+        T* dg = static_cast<T*>(p.dg) + at.b * p.dgs[0] + (t0 + kRows) * p.dgs[1] + c;
+#pragma unroll
+        for (int r = kRows - 1; r >= 0; --r) {
+          const int at4 = r * kRowBytes + ((lane * 4) ^ ((r & 7) << 4));
+          dx -= p.dxs[1], dg -= p.dgs[1];
+          if (r < left) {
+            const V lam = add_(W::open(*reinterpret_cast<const uint32_t*>(rows + 2 * S::kBox + at4)), mu);
+            mu = mul_(a[r], lam);
+            if (c < p.D) {
+              put_word<T>(p, dx, c, INPUT == TTT_SCAN_COMPLEMENT ? mul_(rest[r], lam) : lam);
+              put_word<T>(p, dg, c, gate_grad<GATE>(a[r], rest[r], mul_(lam, d[r])));
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sc.empty[s]);
+    }
+    cur = next;
+  }
+}
+
+// Sequences of at most kShort tokens (new tokens of a stream): one thread per word of
+// channels, no shared memory and nothing to wait for.
+template <class T, int GATE, int INPUT, bool BACKWARD>
+__global__ void __launch_bounds__(128) scan_short_kernel(const __grid_constant__ ScanArgs p) {
+  using W = Word<T>;
+  using V = typename W::V;
+  constexpr int N = W::N;
+  const int words = (p.D + N - 1) / N;
+  const int64_t k = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (k >= int64_t(p.B) * words) return;
+  const int b = int(k / words), c = int(k % words) * N;
+  const int64_t e = int64_t(b) * p.D + c;
+  const int n = int(length_of(p, b));
+  auto load = [&](const void* base, const int64_t(&s)[2], int t) {
+    const T* from = static_cast<const T*>(base) + b * s[0] + t * s[1] + c;
+    if (p.load != kLoad2) return W::open(*reinterpret_cast<const uint32_t*>(from));
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(from);
+    return W::open(N == 2 && c + 1 < p.D ? h[0] | uint32_t(h[1]) << 16 : h[0]);
+  };
+  auto state = [&](const float* from) {
+    float v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = from && c + i < p.D ? from[e + i] : 0.f;
+    return W::make(v);
+  };
+  auto keep = [&](float* to, V v) {
+    if (to)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (c + i < p.D) to[e + i] = v[i];
+  };
+  V st = state(BACKWARD ? p.saved : p.h0);
+  if (!BACKWARD && p.L) keep(p.saved, st);
+  V a[kShort], rest[kShort], d[kShort];
+#pragma unroll
+  for (int r = 0; r < kShort; ++r) {
+    if (r >= n) break;
+    const V g = load(p.g, p.gs, r), x = load(p.x, p.xs, r);
+    gate<T, GATE>(g, a[r], rest[r]);
+    d[r] = INPUT == TTT_SCAN_COMPLEMENT ? sub_(st, x) : st;
+    st = fma_(a[r], st, INPUT == TTT_SCAN_COMPLEMENT ? mul_(rest[r], x) : x);
+    if constexpr (!BACKWARD) put_word<T>(p, static_cast<T*>(p.h) + b * p.hs[0] + r * p.hs[1] + c, c, st);
+  }
+  if constexpr (!BACKWARD) {
+    keep(p.h_last, st);
+  } else {
+    V mu = state(p.dh_last);
+#pragma unroll
+    for (int r = kShort - 1; r >= 0; --r) {
+      if (r >= n) continue;
+      const V lam = add_(load(p.dh, p.dhs, r), mu);
+      mu = mul_(a[r], lam);
+      put_word<T>(p, static_cast<T*>(p.dx) + b * p.dxs[0] + r * p.dxs[1] + c, c,
+                  INPUT == TTT_SCAN_COMPLEMENT ? mul_(rest[r], lam) : lam);
+      put_word<T>(p, static_cast<T*>(p.dg) + b * p.dgs[0] + r * p.dgs[1] + c, c,
+                  gate_grad<GATE>(a[r], rest[r], mul_(lam, d[r])));
+    }
+    keep(p.dh0, mu);
+  }
+}
+
+// Bytes of a call's workspace: the counter, then every tile's map and state.
+struct Space {
+  size_t maps, states, total;
+};
+Space space_of(int64_t tiles, int per_word) {
+  Space s;
+  s.maps = 16;
+  s.states = s.maps + size_t(tiles) * 32 * per_word * 8;
+  s.total = s.states + size_t(tiles) * 32 * per_word * 4;
+  return s;
+}
+
+template <class T, int GATE, int INPUT, bool BACKWARD>
+int launch(ScanArgs& a, const int64_t (*strides)[2], cudaStream_t st) {
+  using S = Shape<T, BACKWARD>;
+  if (a.L <= kShort) {
+    const int64_t n = int64_t(a.B) * ((a.D + S::N - 1) / S::N), grid = (n + 127) / 128;
+    if (grid > 0x7fffffff) return TTT_ERR_UNSUPPORTED;
+    scan_short_kernel<T, GATE, INPUT, BACKWARD><<<unsigned(grid), 128, 0, st>>>(a);
+    return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+  }
+  const auto kernel = scan_tile_kernel<T, GATE, INPUT, BACKWARD>;
+  static OncePerDevice once;
+  const int dev = current_device();
+  if (once.run(dev, [&] {
+        return int(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem));
+      }) != 0)
+    return TTT_ERR_CUDA;
+  CUtensorMap m[3] = {};
+  if (a.load == kLoadTma) {
+    const void* base[3] = {a.g, a.x, a.dh};
+    for (int k = 0; k < S::kTensors; ++k)
+      if (!make_tmap(&m[k], base[k], int(sizeof(T)), a.D, a.L, a.B, strides[k][1], a.B > 1 ? strides[k][0] : 16, S::kTile))
+        a.load = kLoad4;  // rows that TMA takes are on 4 bytes too
+  }
+  const int grid = std::min(2 * sm_count(), a.total);
+  // all ones: nothing published, and a counter whose first answer is -1
+  if (a.counter && cudaMemsetAsync(a.counter, 0xff, space_of(a.total, S::N).total, st) != cudaSuccess)
+    return TTT_ERR_CUDA;
+  kernel<<<grid, kThreads, S::kSmem, st>>>(a, m[0], m[1], m[2]);
+  return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+}
+
+using Launch = int (*)(ScanArgs&, const int64_t (*)[2], cudaStream_t);
+template <class T, bool BACKWARD>
+Launch pick(int gate, int input) {
+  constexpr int P = TTT_SCAN_PLAIN, C = TTT_SCAN_COMPLEMENT;
+  const bool plain = input == TTT_SCAN_PLAIN;
+  if (gate == TTT_GATE_VALUE) return plain ? launch<T, TTT_GATE_VALUE, P, BACKWARD> : launch<T, TTT_GATE_VALUE, C, BACKWARD>;
+  if (gate == TTT_GATE_SIGMOID)
+    return plain ? launch<T, TTT_GATE_SIGMOID, P, BACKWARD> : launch<T, TTT_GATE_SIGMOID, C, BACKWARD>;
+  return plain ? launch<T, TTT_GATE_EXP, P, BACKWARD> : launch<T, TTT_GATE_EXP, C, BACKWARD>;
 }
 
 }  // namespace
@@ -130,6 +799,23 @@ struct ttt_scan {
 namespace {
 
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
+
+int words_of(const ttt_scan* h) { return h->cfg.dtype == TTT_BF16 ? 2 : 1; }
+int64_t up(int64_t n, int64_t d) { return (n + d - 1) / d; }
+int tile_tokens(bool backward) {
+  return backward ? Shape<float, true>::kTile : Shape<float, false>::kTile;
+}
+// tiles of a call, or -1 for more than the counter takes
+int64_t tiles_of(const ttt_scan* h, int32_t B, int64_t L, bool backward) {
+  const __int128 n = __int128(B) * up(h->cfg.D, 32 * words_of(h)) * std::max<int64_t>(up(L, tile_tokens(backward)), 1);
+  return n > (int64_t(1) << 30) ? -1 : int64_t(n);
+}
+// bytes of one direction's workspace: none for sequences of one tile
+size_t space_needed(const ttt_scan* h, int32_t B, int64_t L, bool backward) {
+  if (L <= tile_tokens(backward) || L <= kShort) return 0;
+  const int64_t n = tiles_of(h, B, L, backward);
+  return n < 0 ? 0 : space_of(n, words_of(h)).total;
+}
 
 bool scan_sizes_ok(const ttt_scan* h, int32_t B, int64_t L) { return h && B >= 1 && L >= 0; }
 
@@ -175,14 +861,54 @@ extern "C" int ttt_scan_create(const ttt_scan_config* c, ttt_scan** out) {
 extern "C" void ttt_scan_destroy(ttt_scan* h) { delete h; }
 
 extern "C" size_t ttt_scan_workspace_size(const ttt_scan* h, int32_t B, int64_t L) {
-  (void)h, (void)B, (void)L;
-  return 0;
+  if (!scan_sizes_ok(h, B, L) || L > kMaxTokens) return 0;
+  return std::max(space_needed(h, B, L, false), space_needed(h, B, L, true));
 }
 
 extern "C" size_t ttt_scan_saved_size(const ttt_scan* h, int32_t B, int64_t L) {
   if (!scan_sizes_ok(h, B, L) || L > kMaxTokens) return 0;
-  return size_t(B) * size_t(L) * size_t(h->cfg.D) * 4;
+  return size_t(B) * size_t(up(L, kSave)) * size_t(h->cfg.D) * 4;
 }
+
+namespace {
+
+// the parts of the arguments that both directions share; a status
+int prepare(const ttt_scan* h, bool backward, int32_t B, int64_t L, const RowTensor* in, int nin, const RowTensor* out, int nout,
+            void* workspace, size_t workspace_bytes, unsigned* status, ScanArgs* a) {
+  const bool bf16 = h->cfg.dtype == TTT_BF16;
+  const int64_t tiles = tiles_of(h, B, L, backward);
+  if (L > kShort && tiles < 0) return TTT_ERR_UNSUPPORTED;
+  const size_t need = ttt_scan_workspace_size(h, B, L);
+  if (need && (!workspace || workspace_bytes < need)) return TTT_ERR_WORKSPACE;
+  a->L = L, a->B = B, a->D = h->cfg.D;
+  a->status = status;
+  a->per_col = int32_t(up(L, tile_tokens(backward)));
+  a->kept = int32_t(up(L, kSave));
+  a->cols = int32_t(up(a->D, 32 * words_of(h)));
+  a->total = int32_t(tiles);
+  if (space_needed(h, B, L, backward)) {
+    const Space s = space_of(tiles, words_of(h));
+    char* w = static_cast<char*>(workspace);
+    a->counter = reinterpret_cast<unsigned*>(w);
+    a->maps = reinterpret_cast<uint64_t*>(w + s.maps);
+    a->states = reinterpret_cast<uint32_t*>(w + s.states);
+  }
+  // TMA takes rows on 16 bytes whose dimensions have a stride; 4-byte words take rows on
+  // 4 bytes and whole words (bf16: an even number of channels)
+  const bool whole = !bf16 || a->D % 2 == 0;
+  a->load = whole ? kLoadTma : kLoad2;
+  for (int i = 0; i < nin; ++i) {
+    if (!rows_aligned(in[i], 16) || in[i].stride[1] == 0 || (B > 1 && in[i].stride[0] == 0))
+      a->load = a->load == kLoadTma ? kLoad4 : a->load;
+    if (!rows_aligned(in[i], 4)) a->load = kLoad2;
+  }
+  a->wide = whole;
+  for (int i = 0; i < nout; ++i)
+    if (!rows_aligned(out[i], 4)) a->wide = 0;
+  return TTT_OK;
+}
+
+}  // namespace
 
 extern "C" int ttt_scan_forward(const ttt_scan* h, int32_t B, int64_t L, const void* g, const ttt_strides* gs,
                                 const void* x, const ttt_strides* xs, const float* h0, const int32_t* lengths, void* ho,
@@ -197,20 +923,16 @@ extern "C" int ttt_scan_forward(const ttt_scan* h, int32_t B, int64_t L, const v
   const RowTensor H0 = state(h, B, h0);
   if (!H0.readable() || may_share(H0, out[0]) || may_share(H0, out[2])) return TTT_ERR_INVALID_ARG;
   if (h0 != h_last && may_share(H0, out[1])) return TTT_ERR_INVALID_ARG;
-  if (workspace_bytes < ttt_scan_workspace_size(h, B, L)) return TTT_ERR_WORKSPACE;
-  (void)status;
   ScanArgs a{};
+  const int r = prepare(h, false, B, L, in, 2, out, 1, workspace, workspace_bytes, status, &a);
+  if (r != TTT_OK) return r;
   a.g = g, a.x = x, a.h0 = h0, a.lengths = lengths, a.h = ho, a.h_last = h_last;
   a.saved = static_cast<float*>(saved);
   put_strides(a.gs, gs), put_strides(a.xs, xs), put_strides(a.hs, hs);
-  a.L = L, a.B = B, a.D = h->cfg.D;
-  const int64_t n = int64_t(B) * a.D;
-  const ScanKernel f = h->cfg.dtype == TTT_BF16 ? pick<__nv_bfloat16>(false, h->cfg.gate, h->cfg.input)
-                                                : pick<float>(false, h->cfg.gate, h->cfg.input);
-  const int64_t grid = (n + 127) / 128;
-  if (grid > 0x7fffffff) return TTT_ERR_UNSUPPORTED;
-  f<<<unsigned(grid), 128, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+  const int64_t strides[2][2] = {{gs->batch, gs->token}, {xs->batch, xs->token}};
+  const Launch f = h->cfg.dtype == TTT_BF16 ? pick<__nv_bfloat16, false>(h->cfg.gate, h->cfg.input)
+                                            : pick<float, false>(h->cfg.gate, h->cfg.input);
+  return f(a, strides, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int ttt_scan_backward(const ttt_scan* h, int32_t B, int64_t L, const void* dh, const ttt_strides* dhs,
@@ -227,19 +949,16 @@ extern "C" int ttt_scan_backward(const ttt_scan* h, int32_t B, int64_t L, const 
                           state(h, B, dh_last),   bytes(lengths, size_t(B) * 4), bytes(saved, nsaved)};
   const RowTensor out[] = {rows(h, B, L, dg, dgs), rows(h, B, L, dx, dxs), state(h, B, dh0)};
   if (!is_aligned(lengths, 4) || !apart(in, 6, out, 3)) return TTT_ERR_INVALID_ARG;
-  if (workspace_bytes < ttt_scan_workspace_size(h, B, L)) return TTT_ERR_WORKSPACE;
-  (void)status;
   ScanArgs a{};
+  const RowTensor tiles[] = {in[1], in[2], in[0]};
+  const int r = prepare(h, true, B, L, tiles, 3, out, 2, workspace, workspace_bytes, status, &a);
+  if (r != TTT_OK) return r;
   a.dh = dh, a.g = g, a.x = x, a.dh_last = dh_last, a.lengths = lengths, a.dg = dg, a.dx = dx, a.dh0 = dh0;
   a.saved = static_cast<float*>(const_cast<void*>(saved));
   put_strides(a.dhs, dhs), put_strides(a.gs, gs), put_strides(a.xs, xs), put_strides(a.dgs, dgs),
       put_strides(a.dxs, dxs);
-  a.L = L, a.B = B, a.D = h->cfg.D;
-  const int64_t n = int64_t(B) * a.D;
-  const ScanKernel f = h->cfg.dtype == TTT_BF16 ? pick<__nv_bfloat16>(true, h->cfg.gate, h->cfg.input)
-                                                : pick<float>(true, h->cfg.gate, h->cfg.input);
-  const int64_t grid = (n + 127) / 128;
-  if (grid > 0x7fffffff) return TTT_ERR_UNSUPPORTED;
-  f<<<unsigned(grid), 128, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+  const int64_t strides[3][2] = {{gs->batch, gs->token}, {xs->batch, xs->token}, {dhs->batch, dhs->token}};
+  const Launch f = h->cfg.dtype == TTT_BF16 ? pick<__nv_bfloat16, true>(h->cfg.gate, h->cfg.input)
+                                            : pick<float, true>(h->cfg.gate, h->cfg.input);
+  return f(a, strides, static_cast<cudaStream_t>(stream));
 }
