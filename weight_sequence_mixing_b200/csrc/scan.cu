@@ -14,7 +14,7 @@
 //     a ring of stages (TMA; rows that TMA cannot address, on strides that are no multiple
 //     of 16 bytes, by 4-byte asynchronous copies or plain loads).  Eight sweep a tile's
 //     rows twice: first for the maps, and one tile later, when the states that enter are
-//     there, for the states themselves.  One follows the chain of states from tile to tile.
+//     there, for the states themselves.  Two follow the chain of states from tile to tile, the block's tiles in turn.
 //     So a tile's state is waited for while the next tile's maps are formed, and loads run
 //     on throughout.  The gates are formed in both sweeps: keeping them (8 bytes a value
 //     in registers) was measured, and it holds too few tokens in flight for the chain's
@@ -45,9 +45,9 @@ namespace ttt {
 namespace {
 
 constexpr int kWarps = 8;          // warps that sweep a tile's rows
-constexpr int kChainWarp = 8;      // the warp that follows the chain of states
-constexpr int kFeedWarp = 9;       // the warp that fetches rows
-constexpr int kThreads = 32 * 10;
+constexpr int kChainWarp = 8;      // two warps that follow the chain of states, tile about
+constexpr int kFeedWarp = 10;      // the warp that fetches rows
+constexpr int kThreads = 32 * 11;
 constexpr int kRowBytes = 128;     // a tile's channels: 32 lanes of 4 bytes
 constexpr int kSave = 64;          // tokens from one kept state to the next
 constexpr int kShort = 16;         // longest sequence of the short form
@@ -417,12 +417,16 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
 
   if (warp == kFeedWarp) {
-    int k = 0, turn = 0;
-    for (bool more = true; more; ++turn) {
+    int k = 0;
+    bool more = true;
+    for (int turn = 0, ends = 0; ends < 2; ++turn) {  // an end for each chain warp
       int t = 0;
-      if (lane == 0) t = p.counter ? int(atomicAdd(p.counter, 1u) + 1u) : int(blockIdx.x) + turn * int(gridDim.x);
-      t = __shfl_sync(~0u, t, 0);
-      more = t < p.total;
+      if (more) {
+        if (lane == 0) t = p.counter ? int(atomicAdd(p.counter, 1u) + 1u) : int(blockIdx.x) + turn * int(gridDim.x);
+        t = __shfl_sync(~0u, t, 0);
+        more = t < p.total;
+      }
+      ends += !more;
       Place at{};
       int64_t len = 0, t0 = 0;
       if (more) {
@@ -481,8 +485,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     return;
   }
 
-  if (warp == kChainWarp) {
-    for (int k = 0;; ++k) {
+  if (warp >= kChainWarp) {
+    for (int k = warp - kChainWarp;; k += 2) {
       const int s = k % kStages, par = k & 1;
       if (!wait(&sc.full[s], k / kStages)) return;
       const int t = *(volatile int*)&sc.tile[s];
