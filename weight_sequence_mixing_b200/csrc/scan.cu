@@ -18,7 +18,7 @@
 //     So a tile's state is waited for while the next tile's maps are formed, and loads run
 //     on throughout.  The gates are formed in both sweeps: keeping them (8 bytes a value
 //     in registers) was measured, and it holds too few tokens in flight for the chain's
-//     latency (scene layer of 1029120 tokens, 1024 channels: 5.98 ms, against FWD_MS here).
+//     latency (scene layer of 1029120 tokens, 1024 channels: 5.98 ms, against 1.74 here).
 //   - A warp takes the same channels of a few consecutive tokens; a lane one 4-byte word
 //     of channels of each.
 //   - Tiles are handed out by a counter, tokens first to last, so a tile only waits for
@@ -149,8 +149,9 @@ __device__ __forceinline__ float rcp_fast(float v) {
 }
 
 // a and 1 - a of a lane's values; the complement is formed on its own, so that it keeps
-// its digits where a is close to 1.  bf16 inputs take the hardware's exponential and
-// reciprocal (a few units of 2^-24 off), fp32 ones the library's.
+// its digits where a is close to 1.  bf16 inputs take the hardware's exponential (2^-22
+// off, and 2^-24 of the exponent's size), fp32 ones the library's; the reciprocal is the
+// hardware's, 2^-23 off at most.
 template <class T, int GATE>
 __device__ __forceinline__ void gate(typename Word<T>::V g, typename Word<T>::V& a, typename Word<T>::V& rest) {
   using W = Word<T>;
@@ -167,11 +168,24 @@ __device__ __forceinline__ void gate(typename Word<T>::V g, typename Word<T>::V&
       rest = two(fminf(q[0], 1.f), fminf(q[1], 1.f));
     } else {
       a = e;
-      rest = two(-expm1f(g[0]), -expm1f(g[1]));
+      // 1 - e^g: below 1/2 in size by the series of (1 - e^g) / -g, 2^-26 off at most, which
+      // keeps the digits that the difference loses
+      Two s = W::all(1.f / 362880.f);
+      s = fma_(s, g, W::all(1.f / 40320.f));
+      s = fma_(s, g, W::all(1.f / 5040.f));
+      s = fma_(s, g, W::all(1.f / 720.f));
+      s = fma_(s, g, W::all(1.f / 120.f));
+      s = fma_(s, g, W::all(1.f / 24.f));
+      s = fma_(s, g, W::all(1.f / 6.f));
+      s = fma_(s, g, W::all(0.5f));
+      s = fma_(s, g, W::all(1.f));
+      s = mul_(s, g);
+      const Two f = sub_(W::all(1.f), e);
+      rest = two(fabsf(g[0]) < 0.5f ? -s[0] : f[0], fabsf(g[1]) < 0.5f ? -s[1] : f[1]);
     }
   } else if constexpr (GATE == TTT_GATE_SIGMOID) {  // of e^-|g| in (0, 1]: nothing overflows
     const float e = expf(-fabsf(g.v));
-    const float p = 1.f / (1.f + e), q = e * p;
+    const float p = rcp_fast(1.f + e), q = e * p;
     a.v = g.v < 0.f ? q : p;
     rest.v = g.v < 0.f ? p : q;
   } else {
@@ -198,6 +212,11 @@ __device__ __forceinline__ int64_t length_of(const ScanArgs& p, int b) {
 
 struct Place {
   int b, col, i;  // batch entry, column of channels, tile of the sequence in token order
+};
+struct Job {
+  int t;    // the tile's number as handed out, or -1: no more
+  int len;  // tokens of its sequence
+  Place at;
 };
 template <bool BACKWARD>
 __device__ __forceinline__ Place place_of(const ScanArgs& p, int t) {
@@ -340,43 +359,48 @@ struct Shape {
   static constexpr int kTile = kWarps * kRows;
   static constexpr int kBox = kTile * kRowBytes;  // bytes of one tensor's tile
   static constexpr int kTensors = BACKWARD ? 3 : 2;
-  static constexpr int kStages = 3;
+  static constexpr int kStages = BACKWARD ? 4 : 3;
   static constexpr int kStageBytes = kTensors * kBox;
   struct Scratch {  // behind the stages; two of each by parity of the block's tiles
-    float A[2][kWarps][32 * N], H[2][kWarps][32 * N];  // each warp's map
-    float R[BACKWARD ? 2 : 1][BACKWARD ? kWarps : 1][32 * N];   // backward: its map's (A, R) of mu
-    float in[2][kWarps][32 * N];                                // the state that enters each warp's rows
-    float back[BACKWARD ? 2 : 1][BACKWARD ? kWarps : 1][32 * N];  // backward: the mu that enters
+    float A[2][kWarps][32 * N];   // each warp's map: A,
+    float H[2][kWarps][32 * N];   // and H, then in its place the state that enters the warp's rows
+    float R[BACKWARD ? 2 : 1][BACKWARD ? kWarps : 1][32 * N];  // backward: the map A mu + R, then the mu that enters
     uint64_t full[kStages], empty[kStages];  // a stage's rows are there; are done with
     uint64_t mapped[2], entered[2];          // a tile's maps are there; its states
-    int tile[kStages];                       // the stages' tiles, or -1: no more
+    Job job[kStages];                        // the stages' tiles
     int abort;
   };
   static constexpr int kSmem = 1024 + kStages * kStageBytes + int(sizeof(Scratch));
 };
 
-// One tensor's rows of a tile into shared memory, at the swizzle TMA uses, by one warp
+// One tensor's rows of a tile into shared memory, at the swizzle TMA uses, by one warp.
+// Nothing is read where the size is 0: the word is filled with zero.
 template <class T, int TILE>
 __device__ __forceinline__ void fetch(const ScanArgs& p, const void* base, const int64_t (&s)[2], int b, int c, int64_t t0,
                                       int64_t len, uint8_t* dst) {
   const int lane = threadIdx.x % 32;
-  const T* src = static_cast<const T*>(base) + b * s[0] + c;
-#pragma unroll 8
-  for (int r = 0; r < TILE; ++r) {
-    uint32_t* to = reinterpret_cast<uint32_t*>(dst + r * kRowBytes + ((lane * 4) ^ ((r & 7) << 4)));
-    const bool live = t0 + r < len && c < p.D;
-    const T* from = live ? src + (t0 + r) * s[1] : static_cast<const T*>(base);
-    if (p.load == kLoad4) {  // nothing is read where the size is 0: zero-filled
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(live ? 4 : 0)
+  const int rows = c < p.D ? int(len - t0 < TILE ? len - t0 : TILE) : 0;
+  const T* from = static_cast<const T*>(base) + (rows ? b * s[0] + t0 * s[1] + c : 0);
+  const uint32_t to = smem_u32(dst);
+  if (p.load == kLoad4) {
+#pragma unroll 16
+    for (int r = 0; r < TILE; ++r) {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + r * kRowBytes + ((lane * 4) ^ ((r & 7) << 4))),
+                   "l"(from), "r"(r < rows ? 4 : 0)
                    : "memory");
-    } else {
+      if (r + 1 < rows) from += s[1];
+    }
+  } else {
+#pragma unroll 16
+    for (int r = 0; r < TILE; ++r) {
       uint32_t w = 0;
-      if (live) {
+      if (r < rows) {
         const uint16_t* h = reinterpret_cast<const uint16_t*>(from);
         w = h[0];
         if (Word<T>::N == 2 && c + 1 < p.D) w |= uint32_t(h[1]) << 16;
       }
-      *to = w;
+      if (r + 1 < rows) from += s[1];
+      *reinterpret_cast<uint32_t*>(dst + r * kRowBytes + ((lane * 4) ^ ((r & 7) << 4))) = w;
     }
   }
 }
@@ -417,19 +441,22 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
 
   if (warp == kFeedWarp) {
+    auto hand_out = [&](int turn) {
+      int t = 0;
+      if (lane == 0) t = p.counter ? int(atomicAdd(p.counter, 1u) + 1u) : int(blockIdx.x) + turn * int(gridDim.x);
+      return t;
+    };
     int k = 0;
     bool more = true;
-    for (int turn = 0, ends = 0; ends < 2; ++turn) {  // an end for each chain warp
-      int t = 0;
-      if (more) {
-        if (lane == 0) t = p.counter ? int(atomicAdd(p.counter, 1u) + 1u) : int(blockIdx.x) + turn * int(gridDim.x);
-        t = __shfl_sync(~0u, t, 0);
-        more = t < p.total;
-      }
+    int upcoming = hand_out(0);
+    for (int turn = 1, ends = 0; ends < 2; ++turn) {  // an end for each chain warp
+      const int t = __shfl_sync(~0u, upcoming, 0);
+      more = more && t < p.total;
       ends += !more;
       Place at{};
       int64_t len = 0, t0 = 0;
       if (more) {
+        upcoming = hand_out(turn);  // its answer comes while this tile is fetched
         at = place_of<BACKWARD>(p, t);
         len = length_of(p, at.b);
         t0 = int64_t(at.i) * kTile;
@@ -448,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       const int s = k % kStages;
       if (k >= kStages && !wait(&sc.empty[s], k / kStages - 1)) break;
-      if (lane == 0) sc.tile[s] = more ? t : -1;
+      if (lane == 0) sc.job[s] = Job{more ? t : -1, int(len), at};
       __syncwarp();
       uint8_t* const to = stages + s * S::kStageBytes;
       const int c0 = at.col * 32 * N;
@@ -489,10 +516,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int k = warp - kChainWarp;; k += 2) {
       const int s = k % kStages, par = k & 1;
       if (!wait(&sc.full[s], k / kStages)) return;
-      const int t = *(volatile int*)&sc.tile[s];
+      const Job job = sc.job[s];
+      const int t = job.t;
       if (t < 0) return;
-      const Place at = place_of<BACKWARD>(p, t);
-      const int64_t len = length_of(p, at.b);
+      const Place at = job.at;
+      const int64_t len = job.len;
       const int last = int((len - 1) / kTile);
       const int before = BACKWARD ? last - at.i : at.i;
       const bool wanted = BACKWARD ? at.i > 0 : at.i < last;  // another tile needs this one's state
@@ -515,8 +543,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int w = 0; w < kWarps; ++w)
 #pragma unroll
           for (int v = 0; v < N; ++v) {
-            sc.in[par][w][lane * N + v] = h[v];
+            const float enters = h[v];
             h[v] = apply(sc.A[par][w][lane * N + v], sc.H[par][w][lane * N + v], h[v]);
+            sc.H[par][w][lane * N + v] = enters;
           }
       } else if (!wait(&sc.mapped[par], k / 2)) {
         return;
@@ -553,9 +582,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int v = 0; v < N; ++v) {
           if (BACKWARD)
-            sc.back[par][w][lane * N + v] = st[v];
+            sc.R[par][w][lane * N + v] = st[v];
           else
-            sc.in[par][w][lane * N + v] = st[v];
+            sc.H[par][w][lane * N + v] = st[v];
           if (!BACKWARD && w * kRows % kSave == 0 && p.saved && c + v < p.D &&
               int64_t(at.i) * kTile + w * kRows < len)
             p.saved[(int64_t(at.b) * p.kept + at.i * (kTile / kSave) + w * kRows / kSave) * p.D + c + v] = st[v];
@@ -577,31 +606,41 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 
   // the sweeping warps: the maps of tile k + 1, then the states of tile k
-  int cur = -1;
+  int swizzle[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) swizzle[r] = warp * kRows * kRowBytes + ((lane * 4) ^ (r << 4));
+  Job cur{};
+  cur.t = -1;
   for (int k = -1;; ++k) {
-    int next = -1;
-    if (k < 0 || cur >= 0) {
+    Job next{};
+    next.t = -1;
+    if (k < 0 || cur.t >= 0) {
       const int s = (k + 1) % kStages, par = (k + 1) & 1;
       if (!wait(&sc.full[s], (k + 1) / kStages)) return;
-      next = *(volatile int*)&sc.tile[s];
-      if (next >= 0) {
-        const Place at = place_of<BACKWARD>(p, next);
-        const int64_t left = length_of(p, at.b) - (int64_t(at.i) * kTile + warp * kRows);
-        const uint8_t* const rows = stages + s * S::kStageBytes + warp * kRows * kRowBytes;
+      next = sc.job[s];
+      if (next.t >= 0) {
+        const int left = next.len - (next.at.i * kTile + warp * kRows);
+        const uint8_t* const stage = stages + s * S::kStageBytes;
+        auto word = [&](int tensor, int r) {
+          return W::open(*reinterpret_cast<const uint32_t*>(stage + tensor * S::kBox + (r & ~7) * kRowBytes +
+                                                            (r & 7) * kRowBytes + swizzle[r & 7]));
+        };
         V A = W::all(1.f), H = W::all(0.f), R = W::all(0.f);
+        auto token = [&](int r) {
+          const V g = word(0, r), x = word(1, r);
+          V a, rest;
+          gate<T, GATE>(g, a, rest);
+          H = fma_(a, H, INPUT == TTT_SCAN_COMPLEMENT ? mul_(rest, x) : x);
+          A = mul_(A, a);
+          if (BACKWARD) R = fma_(A, word(2, r), R);
+        };
+        if (left >= kRows) {
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-          const int at4 = r * kRowBytes + ((lane * 4) ^ ((r & 7) << 4));
-          const V g = W::open(*reinterpret_cast<const uint32_t*>(rows + at4));
-          const V x = W::open(*reinterpret_cast<const uint32_t*>(rows + S::kBox + at4));
-          if (r < left) {  // rows behind the end hold anything
-            V a, rest;
-            gate<T, GATE>(g, a, rest);
-            H = fma_(a, H, INPUT == TTT_SCAN_COMPLEMENT ? mul_(rest, x) : x);
-            A = mul_(A, a);
-            if (BACKWARD)
-              R = fma_(A, W::open(*reinterpret_cast<const uint32_t*>(rows + 2 * S::kBox + at4)), R);
-          }
+          for (int r = 0; r < kRows; ++r) token(r);
+        } else {  // rows behind the end hold anything
+#pragma unroll
+          for (int r = 0; r < kRows; ++r)
+            if (r < left) token(r);
         }
 #pragma unroll
         for (int v = 0; v < N; ++v) {
@@ -614,59 +653,80 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     if (k >= 0) {
-      if (cur < 0) return;
+      if (cur.t < 0) return;
       const int s = k % kStages, par = k & 1;
-      const Place at = place_of<BACKWARD>(p, cur);
-      const int64_t t0 = int64_t(at.i) * kTile + warp * kRows;
-      const int64_t left = length_of(p, at.b) - t0;
-      const int c = (at.col * 32 + lane) * N;
-      const uint8_t* const rows = stages + s * S::kStageBytes + warp * kRows * kRowBytes;
+      const int64_t t0 = int64_t(cur.at.i) * kTile + warp * kRows;
+      const int b = cur.at.b;
+      const int left = int(cur.len - t0);
+      const int c = (cur.at.col * 32 + lane) * N;
+      // every row and channel of this warp's part is there, and takes 4-byte stores
+      const bool whole = left >= kRows && (cur.at.col + 1) * 32 * N <= p.D && (N == 1 || p.wide);
+      const uint8_t* const stage = stages + s * S::kStageBytes;
+      auto word = [&](int tensor, int r) {
+        return W::open(*reinterpret_cast<const uint32_t*>(stage + tensor * S::kBox + (r & ~7) * kRowBytes +
+                                                          (r & 7) * kRowBytes + swizzle[r & 7]));
+      };
       if (!wait(&sc.entered[par], k / 2)) return;
       float in[N];
 #pragma unroll
-      for (int v = 0; v < N; ++v) in[v] = sc.in[par][warp][lane * N + v];
+      for (int v = 0; v < N; ++v) in[v] = sc.H[par][warp][lane * N + v];
       V st = W::make(in);
       if constexpr (!BACKWARD) {
-        T* to = static_cast<T*>(p.h) + at.b * p.hs[0] + t0 * p.hs[1] + c;
-#pragma unroll
-        for (int r = 0; r < kRows; ++r, to += p.hs[1]) {
-          const int at4 = r * kRowBytes + ((lane * 4) ^ ((r & 7) << 4));
-          const V g = W::open(*reinterpret_cast<const uint32_t*>(rows + at4));
-          const V x = W::open(*reinterpret_cast<const uint32_t*>(rows + S::kBox + at4));
+        T* to = static_cast<T*>(p.h) + b * p.hs[0] + t0 * p.hs[1] + c;
+        auto token = [&](int r) {
+          const V g = word(0, r), x = word(1, r);
           V a, rest;
           gate<T, GATE>(g, a, rest);
           st = fma_(a, st, INPUT == TTT_SCAN_COMPLEMENT ? mul_(rest, x) : x);
-          if (r < left && c < p.D) put_word<T>(p, to, c, st);
+        };
+        if (whole) {
+#pragma unroll
+          for (int r = 0; r < kRows; ++r, to += p.hs[1]) {
+            token(r);
+            *reinterpret_cast<uint32_t*>(to) = W::close(st);
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < kRows; ++r, to += p.hs[1]) {
+            token(r);
+            if (r < left && c < p.D) put_word<T>(p, to, c, st);
+          }
         }
       } else {
         // h_{t-1} (less x_t) of the rows first to last, then the gradients last to first
         V a[kRows], rest[kRows], d[kRows];
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
-          const int at4 = r * kRowBytes + ((lane * 4) ^ ((r & 7) << 4));
-          const V g = W::open(*reinterpret_cast<const uint32_t*>(rows + at4));
-          const V x = W::open(*reinterpret_cast<const uint32_t*>(rows + S::kBox + at4));
+          const V g = word(0, r), x = word(1, r);
           gate<T, GATE>(g, a[r], rest[r]);
           d[r] = INPUT == TTT_SCAN_COMPLEMENT ? sub_(st, x) : st;
           st = fma_(a[r], st, INPUT == TTT_SCAN_COMPLEMENT ? mul_(rest[r], x) : x);
         }
 #pragma unroll
-        for (int v = 0; v < N; ++v) in[v] = sc.back[par][warp][lane * N + v];
+        for (int v = 0; v < N; ++v) in[v] = sc.R[par][warp][lane * N + v];
         V mu = W::make(in);
-        T* dx = static_cast<T*>(p.dx) + at.b * p.dxs[0] + (t0 + kRows) * p.dxs[1] + c;
-        T* dg = static_cast<T*>(p.dg) + at.b * p.dgs[0] + (t0 + kRows) * p.dgs[1] + c;
+        T* dx = static_cast<T*>(p.dx) + b * p.dxs[0] + t0 * p.dxs[1] + c;
+        T* dg = static_cast<T*>(p.dg) + b * p.dgs[0] + t0 * p.dgs[1] + c;
+        dx += (kRows - 1) * p.dxs[1], dg += (kRows - 1) * p.dgs[1];
+        if (whole) {
 #pragma unroll
-        for (int r = kRows - 1; r >= 0; --r) {
-          const int at4 = r * kRowBytes + ((lane * 4) ^ ((r & 7) << 4));
-          dx -= p.dxs[1], dg -= p.dgs[1];
-          if (r < left) {
-            const V lam = add_(W::open(*reinterpret_cast<const uint32_t*>(rows + 2 * S::kBox + at4)), mu);
+          for (int r = kRows - 1; r >= 0; --r, dx -= p.dxs[1], dg -= p.dgs[1]) {
+            const V lam = add_(word(2, r), mu);
             mu = mul_(a[r], lam);
-            if (c < p.D) {
-              put_word<T>(p, dx, c, INPUT == TTT_SCAN_COMPLEMENT ? mul_(rest[r], lam) : lam);
-              put_word<T>(p, dg, c, gate_grad<GATE>(a[r], rest[r], mul_(lam, d[r])));
-            }
+            *reinterpret_cast<uint32_t*>(dx) = W::close(INPUT == TTT_SCAN_COMPLEMENT ? mul_(rest[r], lam) : lam);
+            *reinterpret_cast<uint32_t*>(dg) = W::close(gate_grad<GATE>(a[r], rest[r], mul_(lam, d[r])));
           }
+        } else {
+#pragma unroll
+          for (int r = kRows - 1; r >= 0; --r, dx -= p.dxs[1], dg -= p.dgs[1])
+            if (r < left) {
+              const V lam = add_(word(2, r), mu);
+              mu = mul_(a[r], lam);
+              if (c < p.D) {
+                put_word<T>(p, dx, c, INPUT == TTT_SCAN_COMPLEMENT ? mul_(rest[r], lam) : lam);
+                put_word<T>(p, dg, c, gate_grad<GATE>(a[r], rest[r], mul_(lam, d[r])));
+              }
+            }
         }
       }
       __syncwarp();
