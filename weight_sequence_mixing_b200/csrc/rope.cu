@@ -7,10 +7,12 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <new>
 
 #include "op_checks.h"
+#include "ttt_plan.cuh"
 
 namespace ttt {
 namespace {
@@ -31,42 +33,210 @@ struct RopeArgs {
   int32_t B, H, d, axes, pairs;
   int32_t pos_f32, interleaved;
   float sign;
+  int32_t units, items;       // vectors of pairs of a token; with those that are only copied
+  int32_t lanes, rows;        // a block's items and tokens
+  int32_t item_blocks, head_groups, heads;  // heads of a thread
 };
 
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-
-// One thread per pair, and per channel that is only copied.
 template <class T>
-__global__ void rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopeTable tab) {
-  const int items = a.d - a.pairs;
-  const int64_t total = int64_t(a.B) * a.H * a.N * items;
-  for (int64_t k = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; k < total; k += int64_t(gridDim.x) * blockDim.x) {
-    const int i = int(k % items);
-    const int64_t r = k / items;
-    const int64_t n = r % a.N;
-    const int64_t bh = r / a.N;
-    const int h = int(bh % a.H), b = int(bh / a.H);
-    const T* x = static_cast<const T*>(a.x) + b * a.xs[0] + h * a.xs[1] + n * a.xs[2];
-    T* y = static_cast<T*>(a.y) + b * a.ys[0] + h * a.ys[1] + n * a.ys[2];
-    if (i >= a.pairs) {
-      y[a.pairs + i] = x[a.pairs + i];
-      continue;
-    }
-    const int64_t at = b * a.pos_batch + n * a.axes + tab.axis[i];
-    const double p = a.pos_f32 ? double(static_cast<const float*>(a.pos)[at])
-                               : double(static_cast<const int*>(a.pos)[at]);
-    const double turns = p * tab.turns[i];
-    float sn, cs;
-    sincospif(2.f * float(turns - rint(turns)), &sn, &cs);
-    sn *= a.sign;
-    const int ip = a.interleaved ? 2 * i : i, iq = a.interleaved ? 2 * i + 1 : i + a.pairs;
-    const float u = to_f(x[ip]), v = to_f(x[iq]);
-    put(y + ip, u * cs - v * sn);
-    put(y + iq, v * cs + u * sn);
+__device__ __forceinline__ void open_word(uint32_t w, float (&v)[4 / sizeof(T)]) {
+  if constexpr (sizeof(T) == 4) {
+    v[0] = __uint_as_float(w);
+  } else {
+    v[0] = __uint_as_float(w << 16);
+    v[1] = __uint_as_float(w & 0xffff0000u);
   }
+}
+template <class T>
+__device__ __forceinline__ uint32_t close_word(const float (&v)[4 / sizeof(T)]) {
+  if constexpr (sizeof(T) == 4) {
+    return __float_as_uint(v[0]);
+  } else {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(v[0], v[1]);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  }
+}
+
+// BYTES of consecutive channels
+template <class T, int BYTES>
+struct Vec {
+  static constexpr int N = BYTES / sizeof(T);
+  static constexpr int kWords = (BYTES + 3) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (BYTES == 16) {
+      const uint4 q = *reinterpret_cast<const uint4*>(p);
+      w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+    } else if constexpr (BYTES == 8) {
+      const uint2 q = *reinterpret_cast<const uint2*>(p);
+      w[0] = q.x, w[1] = q.y;
+    } else if constexpr (BYTES == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+      w[0] = *reinterpret_cast<const uint16_t*>(p);
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (BYTES == 16)
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (BYTES == 8)
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else if constexpr (BYTES == 4)
+      *reinterpret_cast<uint32_t*>(p) = w[0];
+    else
+      *reinterpret_cast<uint16_t*>(p) = uint16_t(w[0]);
+  }
+  __device__ __forceinline__ void open(float (&v)[N]) const {
+    if constexpr (BYTES == 2) {
+      v[0] = __uint_as_float(w[0] << 16);
+    } else {
+      constexpr int K = 4 / sizeof(T);
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        float u[K];
+        open_word<T>(w[i], u);
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[i * K + k] = u[k];
+      }
+    }
+  }
+  __device__ __forceinline__ void close(const float (&v)[N]) {
+    if constexpr (BYTES == 2) {
+      w[0] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
+    } else {
+      constexpr int K = 4 / sizeof(T);
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        float u[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) u[k] = v[i * K + k];
+        w[i] = close_word<T>(u);
+      }
+    }
+  }
+};
+
+// A thread owns the same few pairs of every head (or channels that are only copied) and
+// walks over tokens, so its frequencies stay in registers and each angle is formed once
+// for all heads.  Bound by HBM: x is read and y written once, in vectors of BYTES.
+//   ONE: the two channels of a pair lie in one vector (interleaved); else in two.
+// bf16 takes the hardware's sine and cosine (2^-21.2 off on [-pi, pi], far below the
+// output's 2^-9), fp32 sincospif.
+constexpr int kHeadsAtOnce = 4;
+template <class T, int BYTES, bool ONE>
+__global__ void __launch_bounds__(256)
+    rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopeTable tab) {
+  using X = Vec<T, BYTES>;
+  constexpr int P = ONE ? X::N / 2 : X::N;  // pairs of a thread
+  const int item = blockIdx.x % a.item_blocks * a.lanes + threadIdx.x % a.lanes;
+  const int row = threadIdx.x / a.lanes;
+  if (row >= a.rows || item >= a.items) return;
+  const int b = blockIdx.y / a.head_groups, h0 = blockIdx.y % a.head_groups * a.heads;
+  const int heads = min(a.heads, a.H - h0);
+  const T* const x = static_cast<const T*>(a.x) + b * a.xs[0] + h0 * a.xs[1];
+  T* const y = static_cast<T*>(a.y) + b * a.ys[0] + h0 * a.ys[1];
+  const int64_t n0 = int64_t(blockIdx.x / a.item_blocks) * a.rows + row;
+  const int64_t hop = int64_t(gridDim.x / a.item_blocks) * a.rows;
+
+  if (item >= a.units) {  // channels behind the pairs
+    const int c = 2 * a.pairs + (item - a.units) * X::N;
+    for (int64_t n = n0; n < a.N; n += hop)
+      for (int h = 0; h < heads; ++h) {
+        X v;
+        v.load(x + h * a.xs[1] + n * a.xs[2] + c);
+        v.store(y + h * a.ys[1] + n * a.ys[2] + c);
+      }
+    return;
+  }
+  const int i0 = item * P;
+  const int cp = a.interleaved ? 2 * i0 : i0, cq = a.interleaved ? 2 * i0 + 1 : i0 + a.pairs;
+  double turns[P];
+  int axis[P];
+#pragma unroll
+  for (int k = 0; k < P; ++k) {
+    turns[k] = tab.turns[i0 + k];
+    axis[k] = tab.axis[i0 + k];
+  }
+  for (int64_t n = n0; n < a.N; n += hop) {
+    float sn[P], cs[P];
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      const int64_t at = b * a.pos_batch + n * a.axes + axis[k];
+      const double pos = a.pos_f32 ? double(__ldg(static_cast<const float*>(a.pos) + at))
+                                   : double(__ldg(static_cast<const int*>(a.pos) + at));
+      const double t = pos * turns[k];
+      const float f = float(t - rint(t));
+      if constexpr (sizeof(T) == 2) {
+        const float r = f * 6.2831853071795865f;
+        sn[k] = __sinf(r);
+        cs[k] = __cosf(r);
+      } else {
+        sincospif(2.f * f, &sn[k], &cs[k]);
+      }
+      sn[k] *= a.sign;
+    }
+    for (int h = 0; h < heads; h += kHeadsAtOnce) {
+      X p[kHeadsAtOnce], q[kHeadsAtOnce];
+#pragma unroll
+      for (int e = 0; e < kHeadsAtOnce; ++e)
+        if (h + e < heads) {
+          const T* from = x + (h + e) * a.xs[1] + n * a.xs[2];
+          p[e].load(from + cp);
+          if (!ONE) q[e].load(from + cq);
+        }
+#pragma unroll
+      for (int e = 0; e < kHeadsAtOnce; ++e)
+        if (h + e < heads) {
+          T* to = y + (h + e) * a.ys[1] + n * a.ys[2];
+          float u[X::N], v[X::N];
+          p[e].open(u);
+          if constexpr (ONE) {
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+              v[2 * k] = u[2 * k] * cs[k] - u[2 * k + 1] * sn[k];
+              v[2 * k + 1] = u[2 * k + 1] * cs[k] + u[2 * k] * sn[k];
+            }
+            p[e].close(v);
+            p[e].store(to + cp);
+          } else {
+            q[e].open(v);
+            float yp[X::N], yq[X::N];
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+              yp[k] = u[k] * cs[k] - v[k] * sn[k];
+              yq[k] = v[k] * cs[k] + u[k] * sn[k];
+            }
+            p[e].close(yp);
+            q[e].close(yq);
+            p[e].store(to + cp);
+            q[e].store(to + cq);
+          }
+        }
+    }
+  }
+}
+
+template <class T, int BYTES, bool ONE>
+int launch(RopeArgs& a, const RopeTable& tab, bool copy, cudaStream_t st) {
+  constexpr int V = BYTES / int(sizeof(T)), P = ONE ? V / 2 : V;
+  a.units = a.pairs / P;
+  a.items = a.units + (copy ? (a.d - 2 * a.pairs) / V : 0);
+  a.item_blocks = (a.items + 127) / 128;
+  a.lanes = (a.items + a.item_blocks - 1) / a.item_blocks;
+  a.rows = 256 / a.lanes;
+  // all heads in one thread share its angles; fewer where that would leave SMs idle
+  const int64_t row_blocks = (a.N + a.rows - 1) / a.rows;
+  const int64_t enough = int64_t(sm_count()) * 4;
+  a.heads = a.H;
+  auto blocks = [&] { return row_blocks * a.item_blocks * a.B * ((a.H + a.heads - 1) / a.heads); };
+  while (a.heads > 1 && blocks() < enough) a.heads = (a.heads + 1) / 2;
+  a.head_groups = (a.H + a.heads - 1) / a.heads;
+  const int64_t gy = int64_t(a.B) * a.head_groups;
+  if (gy > 65535) return TTT_ERR_UNSUPPORTED;
+  const int64_t most = std::max<int64_t>(1, int64_t(sm_count()) * 16 / (a.item_blocks * gy));
+  const int64_t gx = std::min(row_blocks, most) * a.item_blocks;
+  rope_kernel<T, BYTES, ONE><<<dim3(unsigned(gx), unsigned(gy)), 256, 0, st>>>(a, tab);
+  return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
 }
 
 }  // namespace
@@ -137,14 +307,26 @@ extern "C" int ttt_rope_apply(const ttt_rope* h, int32_t B, int32_t H, int64_t N
   a.pos_f32 = pos_dtype == TTT_POS_F32;
   a.interleaved = c.pairing == TTT_ROPE_INTERLEAVED;
   a.sign = inverse ? -1.f : 1.f;
-  const __int128 items = __int128(B) * H * N * (c.d - h->pairs);
-  if (items > (__int128(1) << 60)) return TTT_ERR_UNSUPPORTED;
-  const int64_t blocks = (int64_t(items) + 255) / 256;
-  const int grid = int(blocks < (1 << 20) ? blocks : (1 << 20));
+  // the widest vectors that rows, pairs and the channels behind them are whole numbers of
+  const bool copy = x != y && c.d > 2 * h->pairs;
+  const int part = a.interleaved ? 2 * h->pairs : h->pairs, behind = copy ? c.d - 2 * h->pairs : 0;
+  int wide = 16;
+  while (wide > e && (part * e % wide || behind * e % wide || !rows_aligned(X, wide) || !rows_aligned(Y, wide))) wide /= 2;
+  const bool one = a.interleaved && wide > e;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (e == 2)
-    rope_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a, h->tab);
-  else
-    rope_kernel<float><<<grid, 256, 0, st>>>(a, h->tab);
-  return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+  if (e == 2) {
+    using T = __nv_bfloat16;
+    if (one)
+      return wide == 16 ? launch<T, 16, true>(a, h->tab, copy, st)
+             : wide == 8 ? launch<T, 8, true>(a, h->tab, copy, st)
+                         : launch<T, 4, true>(a, h->tab, copy, st);
+    return wide == 16 ? launch<T, 16, false>(a, h->tab, copy, st)
+           : wide == 8 ? launch<T, 8, false>(a, h->tab, copy, st)
+           : wide == 4 ? launch<T, 4, false>(a, h->tab, copy, st)
+                       : launch<T, 2, false>(a, h->tab, copy, st);
+  }
+  if (one) return wide == 16 ? launch<float, 16, true>(a, h->tab, copy, st) : launch<float, 8, true>(a, h->tab, copy, st);
+  return wide == 16 ? launch<float, 16, false>(a, h->tab, copy, st)
+         : wide == 8 ? launch<float, 8, false>(a, h->tab, copy, st)
+                     : launch<float, 4, false>(a, h->tab, copy, st);
 }
