@@ -1,9 +1,11 @@
 // Rotary positions with several axes (ttt_ops.h, ttt_rope_*).
 //
-// Pair i of a head belongs to one axis and turns by phi = p_axis * theta_i.  In
-// turns, phi / 2 pi = p * (theta_i / 2 pi): the product is formed in 64 bits and its
-// whole turns are taken off there, since in 32 bits it is off by p 2^-24 turns (a
-// position of 10^6 would lose three digits of the angle).
+// Pair i of a head belongs to one axis and turns by phi = p_axis * theta_i.  The angle is
+// formed in whole turns, phi / 2 pi = p * (theta_i / 2 pi), of which only the fraction
+// counts.  For an integer p that is exact arithmetic modulo 2^64: with theta_i / 2 pi as a
+// 64-bit fraction, the low 64 bits of the product are the turn.  For an fp32 p the product
+// and its reduction are in fp64.  (In 32 bits the product is off by p 2^-24 turns: a
+// position of 10^6 would lose three digits of the angle.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -17,10 +19,11 @@
 namespace ttt {
 namespace {
 
-constexpr double kTwoPi = 6.283185307179586476925286766559;
+constexpr long double kTwoPi = 6.283185307179586476925286766559L;
 
 struct RopeTable {
-  double turns[TTT_ROPE_MAX_PAIRS];  // theta_i / 2 pi
+  double turns[TTT_ROPE_MAX_PAIRS];      // theta_i / 2 pi
+  uint64_t fraction[TTT_ROPE_MAX_PAIRS]; // its fraction in units of 2^-64
   unsigned char axis[TTT_ROPE_MAX_PAIRS];
 };
 
@@ -33,9 +36,11 @@ struct RopeArgs {
   int32_t B, H, d, axes, pairs;
   int32_t pos_f32, interleaved;
   float sign;
-  int32_t units, items;       // vectors of pairs of a token; with those that are only copied
-  int32_t lanes, rows;        // a block's items and tokens
-  int32_t item_blocks, head_groups, heads;  // heads of a thread
+  int32_t units, items;         // vectors of pairs of a token; with those that are only copied
+  int32_t lanes, rows;          // a block's items, and its tokens at a time
+  int32_t item_blocks, head_groups;
+  int64_t tiles;                // of tokens, times head groups and batch entries
+  int64_t row_tiles;            // of tokens
 };
 
 template <class T>
@@ -116,127 +121,158 @@ struct Vec {
   }
 };
 
-// A thread owns the same few pairs of every head (or channels that are only copied) and
-// walks over tokens, so its frequencies stay in registers and each angle is formed once
-// for all heads.  Bound by HBM: x is read and y written once, in vectors of BYTES.
+// A thread owns a vector of pairs (or of channels that are only copied) of every token: its
+// frequencies stay in registers while it walks over tiles of (token, head) steps.  Of a
+// tile it first issues all loads, then forms each token's angles once for its HEADS heads,
+// turns and stores.  Bound by HBM (x read, y written once); what that takes is bytes in
+// flight, here 64 to 128 a thread and 768 threads an SM.
 //   ONE: the two channels of a pair lie in one vector (interleaved); else in two.
 // bf16 takes the hardware's sine and cosine (2^-21.2 off on [-pi, pi], far below the
 // output's 2^-9), fp32 sincospif.
-constexpr int kHeadsAtOnce = 4;
-template <class T, int BYTES, bool ONE>
-__global__ void __launch_bounds__(256)
+// Measured against this (196608 tokens x 2 heads x 512 bf16, 139 us; the copy of as many bytes 123): angles in fp64 and
+// one (token, heads) step ahead, 200 us; angles of a tile shared in shared memory, 211 us.
+template <class T, int BYTES, bool ONE, int HEADS, bool POS_F32>
+__global__ void __launch_bounds__(256, ONE ? 3 : 2)
     rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopeTable tab) {
   using X = Vec<T, BYTES>;
   constexpr int P = ONE ? X::N / 2 : X::N;  // pairs of a thread
+  constexpr int kTokens = (ONE || BYTES < 16 ? 8 : 4) / HEADS;
   const int item = blockIdx.x % a.item_blocks * a.lanes + threadIdx.x % a.lanes;
   const int row = threadIdx.x / a.lanes;
   if (row >= a.rows || item >= a.items) return;
-  const int b = blockIdx.y / a.head_groups, h0 = blockIdx.y % a.head_groups * a.heads;
-  const int heads = min(a.heads, a.H - h0);
-  const T* const x = static_cast<const T*>(a.x) + b * a.xs[0] + h0 * a.xs[1];
-  T* const y = static_cast<T*>(a.y) + b * a.ys[0] + h0 * a.ys[1];
-  const int64_t n0 = int64_t(blockIdx.x / a.item_blocks) * a.rows + row;
-  const int64_t hop = int64_t(gridDim.x / a.item_blocks) * a.rows;
-
-  if (item >= a.units) {  // channels behind the pairs
-    const int c = 2 * a.pairs + (item - a.units) * X::N;
-    for (int64_t n = n0; n < a.N; n += hop)
-      for (int h = 0; h < heads; ++h) {
-        X v;
-        v.load(x + h * a.xs[1] + n * a.xs[2] + c);
-        v.store(y + h * a.ys[1] + n * a.ys[2] + c);
-      }
-    return;
-  }
-  const int i0 = item * P;
-  const int cp = a.interleaved ? 2 * i0 : i0, cq = a.interleaved ? 2 * i0 + 1 : i0 + a.pairs;
-  double turns[P];
+  // copied channels take the same walk as pairs, so that the lanes of a warp stay together
+  const bool rotates = item < a.units;
+  const int i0 = rotates ? item * P : 0;
+  const int cp = !rotates ? 2 * a.pairs + (item - a.units) * X::N : a.interleaved ? 2 * i0 : i0;
+  const int cq = a.interleaved ? 2 * i0 + 1 : i0 + a.pairs;
+  uint64_t freq[P];  // turns a position, as a 64-bit fraction or (fp32 positions) an fp64
   int axis[P];
 #pragma unroll
   for (int k = 0; k < P; ++k) {
-    turns[k] = tab.turns[i0 + k];
+    freq[k] = POS_F32 ? uint64_t(__double_as_longlong(tab.turns[i0 + k])) : tab.fraction[i0 + k];
     axis[k] = tab.axis[i0 + k];
+    // held in registers: read again at each use, the lanes' different places in constant
+    // memory come one after another (575 us for the views below)
+    asm volatile("" : "+l"(freq[k]), "+r"(axis[k]));
   }
-  for (int64_t n = n0; n < a.N; n += hop) {
-    float sn[P], cs[P];
+  const bool one_axis = axis[0] == axis[P - 1];
+  const int hop = gridDim.x / a.item_blocks;
+  for (int64_t tile = blockIdx.x / a.item_blocks; tile < a.tiles; tile += hop) {
+    const int64_t bh = tile / a.row_tiles;
+    const int b = int(bh / a.head_groups), h0 = int(bh % a.head_groups) * HEADS;
+    const int64_t n0 = (tile - bh * a.row_tiles) * (kTokens * a.rows) + row;
+    X p[kTokens][HEADS], q[kTokens][HEADS];
+    int word[kTokens];  // the positions of the first pair, as they are stored
+    {
+      const int* pos = static_cast<const int*>(a.pos) + b * a.pos_batch + n0 * a.axes;
+      const T* x = static_cast<const T*>(a.x) + b * a.xs[0] + h0 * a.xs[1] + n0 * a.xs[2];
 #pragma unroll
-    for (int k = 0; k < P; ++k) {
-      const int64_t at = b * a.pos_batch + n * a.axes + axis[k];
-      const double pos = a.pos_f32 ? double(__ldg(static_cast<const float*>(a.pos) + at))
-                                   : double(__ldg(static_cast<const int*>(a.pos) + at));
-      const double t = pos * turns[k];
-      const float f = float(t - rint(t));
-      if constexpr (sizeof(T) == 2) {
-        const float r = f * 6.2831853071795865f;
-        sn[k] = __sinf(r);
-        cs[k] = __cosf(r);
-      } else {
-        sincospif(2.f * f, &sn[k], &cs[k]);
+      for (int g = 0; g < kTokens; ++g) {
+        if (n0 + g * a.rows < a.N) {
+#pragma unroll
+          for (int h = 0; h < HEADS; ++h)
+            if (h0 + h < a.H) {
+              p[g][h].load(x + h * a.xs[1] + cp);
+              if (!ONE && rotates) q[g][h].load(x + h * a.xs[1] + cq);
+            }
+          word[g] = __ldg(pos + axis[0]);
+        }
+        x += a.rows * a.xs[2];
+        pos += a.rows * a.axes;
       }
-      sn[k] *= a.sign;
     }
-    for (int h = 0; h < heads; h += kHeadsAtOnce) {
-      X p[kHeadsAtOnce], q[kHeadsAtOnce];
+    const int* pos = static_cast<const int*>(a.pos) + b * a.pos_batch + n0 * a.axes;
+    T* y = static_cast<T*>(a.y) + b * a.ys[0] + h0 * a.ys[1] + n0 * a.ys[2];
 #pragma unroll
-      for (int e = 0; e < kHeadsAtOnce; ++e)
-        if (h + e < heads) {
-          const T* from = x + (h + e) * a.xs[1] + n * a.xs[2];
-          p[e].load(from + cp);
-          if (!ONE) q[e].load(from + cq);
+    for (int g = 0; g < kTokens; ++g, y += a.rows * a.ys[2], pos += a.rows * a.axes) {
+      if (n0 + g * a.rows >= a.N) break;
+      float cs[P], sn[P];
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        const int w = k == 0 || one_axis ? word[g] : __ldg(pos + axis[k]);
+        float f;  // the turn, in [-1/2, 1/2]
+        if (POS_F32) {
+          const double v = double(__int_as_float(w)) * __longlong_as_double(int64_t(freq[k]));
+          f = float(v - rint(v));
+        } else {
+          f = float(int(uint64_t(int64_t(w)) * freq[k] >> 32)) * 0x1p-32f;
         }
+        if constexpr (sizeof(T) == 2) {
+          const float r = f * 6.2831853071795865f;
+          sn[k] = __sinf(r);
+          cs[k] = __cosf(r);
+        } else {
+          sincospif(2.f * f, &sn[k], &cs[k]);
+        }
+        sn[k] *= a.sign;
+      }
 #pragma unroll
-      for (int e = 0; e < kHeadsAtOnce; ++e)
-        if (h + e < heads) {
-          T* to = y + (h + e) * a.ys[1] + n * a.ys[2];
-          float u[X::N], v[X::N];
-          p[e].open(u);
-          if constexpr (ONE) {
+      for (int h = 0; h < HEADS; ++h) {
+        if (h0 + h >= a.H) break;
+        T* const to = y + h * a.ys[1];
+        if (!rotates) {
+          p[g][h].store(to + cp);
+          continue;
+        }
+        float u[X::N], v[X::N];
+        p[g][h].open(u);
+        if constexpr (ONE) {
 #pragma unroll
-            for (int k = 0; k < P; ++k) {
-              v[2 * k] = u[2 * k] * cs[k] - u[2 * k + 1] * sn[k];
-              v[2 * k + 1] = u[2 * k + 1] * cs[k] + u[2 * k] * sn[k];
-            }
-            p[e].close(v);
-            p[e].store(to + cp);
-          } else {
-            q[e].open(v);
-            float yp[X::N], yq[X::N];
-#pragma unroll
-            for (int k = 0; k < P; ++k) {
-              yp[k] = u[k] * cs[k] - v[k] * sn[k];
-              yq[k] = v[k] * cs[k] + u[k] * sn[k];
-            }
-            p[e].close(yp);
-            q[e].close(yq);
-            p[e].store(to + cp);
-            q[e].store(to + cq);
+          for (int k = 0; k < P; ++k) {
+            v[2 * k] = u[2 * k] * cs[k] - u[2 * k + 1] * sn[k];
+            v[2 * k + 1] = u[2 * k + 1] * cs[k] + u[2 * k] * sn[k];
           }
+          p[g][h].close(v);
+          p[g][h].store(to + cp);
+        } else {
+          q[g][h].open(v);
+          float yp[X::N], yq[X::N];
+#pragma unroll
+          for (int k = 0; k < P; ++k) {
+            yp[k] = u[k] * cs[k] - v[k] * sn[k];
+            yq[k] = v[k] * cs[k] + u[k] * sn[k];
+          }
+          p[g][h].close(yp);
+          q[g][h].close(yq);
+          p[g][h].store(to + cp);
+          q[g][h].store(to + cq);
         }
+      }
     }
   }
 }
 
-template <class T, int BYTES, bool ONE>
+template <class T, int BYTES, bool ONE, int HEADS>
 int launch(RopeArgs& a, const RopeTable& tab, bool copy, cudaStream_t st) {
   constexpr int V = BYTES / int(sizeof(T)), P = ONE ? V / 2 : V;
+  constexpr int kTokens = (ONE || BYTES < 16 ? 8 : 4) / HEADS;
   a.units = a.pairs / P;
   a.items = a.units + (copy ? (a.d - 2 * a.pairs) / V : 0);
-  a.item_blocks = (a.items + 127) / 128;
+  a.item_blocks = (a.items + 255) / 256;
   a.lanes = (a.items + a.item_blocks - 1) / a.item_blocks;
   a.rows = 256 / a.lanes;
-  // all heads in one thread share its angles; fewer where that would leave SMs idle
-  const int64_t row_blocks = (a.N + a.rows - 1) / a.rows;
-  const int64_t enough = int64_t(sm_count()) * 4;
-  a.heads = a.H;
-  auto blocks = [&] { return row_blocks * a.item_blocks * a.B * ((a.H + a.heads - 1) / a.heads); };
-  while (a.heads > 1 && blocks() < enough) a.heads = (a.heads + 1) / 2;
-  a.head_groups = (a.H + a.heads - 1) / a.heads;
-  const int64_t gy = int64_t(a.B) * a.head_groups;
-  if (gy > 65535) return TTT_ERR_UNSUPPORTED;
-  const int64_t most = std::max<int64_t>(1, int64_t(sm_count()) * 16 / (a.item_blocks * gy));
-  const int64_t gx = std::min(row_blocks, most) * a.item_blocks;
-  rope_kernel<T, BYTES, ONE><<<dim3(unsigned(gx), unsigned(gy)), 256, 0, st>>>(a, tab);
+  a.head_groups = (a.H + HEADS - 1) / HEADS;
+  a.row_tiles = (a.N + kTokens * a.rows - 1) / (kTokens * a.rows);
+  a.tiles = a.row_tiles * a.head_groups * a.B;
+  const int64_t grid = std::min(a.tiles, std::max<int64_t>(1, int64_t(sm_count()) * (ONE ? 3 : 2) / a.item_blocks)) * a.item_blocks;
+  if (a.pos_f32)
+    rope_kernel<T, BYTES, ONE, HEADS, true><<<unsigned(grid), 256, 0, st>>>(a, tab);
+  else
+    rope_kernel<T, BYTES, ONE, HEADS, false><<<unsigned(grid), 256, 0, st>>>(a, tab);
   return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+}
+
+// Heads of a thread: those that share its angles, the most that leave no more than one of
+// all heads' places empty.  Narrow vectors have one form.
+template <class T, int BYTES, bool ONE>
+int launch_heads(RopeArgs& a, const RopeTable& tab, bool copy, cudaStream_t st) {
+  if constexpr (BYTES < 16) {
+    return launch<T, BYTES, ONE, 2>(a, tab, copy, st);
+  } else {
+    if (a.H == 1) return launch<T, BYTES, ONE, 1>(a, tab, copy, st);
+    if (a.H % 4 == 0 || a.H % 4 == 3) return launch<T, BYTES, ONE, 4>(a, tab, copy, st);
+    return launch<T, BYTES, ONE, 2>(a, tab, copy, st);
+  }
 }
 
 }  // namespace
@@ -270,7 +306,9 @@ extern "C" int ttt_rope_create(const ttt_rope_config* c, ttt_rope** out) {
   int at = 0;
   for (int a = 0; a < c->axes; ++a)
     for (int j = 0; j < c->pairs[a]; ++j, ++at) {
-      h->tab.turns[at] = std::pow(c->base[a], -double(j) / c->pairs[a]) / kTwoPi;
+      const long double turns = powl(c->base[a], -static_cast<long double>(j) / c->pairs[a]) / kTwoPi;
+      h->tab.turns[at] = double(turns);
+      h->tab.fraction[at] = static_cast<uint64_t>(ldexpl(turns - floorl(turns), 64));
       h->tab.axis[at] = static_cast<unsigned char>(a);
     }
   *out = h;
@@ -307,6 +345,7 @@ extern "C" int ttt_rope_apply(const ttt_rope* h, int32_t B, int32_t H, int64_t N
   a.pos_f32 = pos_dtype == TTT_POS_F32;
   a.interleaved = c.pairing == TTT_ROPE_INTERLEAVED;
   a.sign = inverse ? -1.f : 1.f;
+  if (__int128(B) * H * N > (__int128(1) << 60)) return TTT_ERR_UNSUPPORTED;
   // the widest vectors that rows, pairs and the channels behind them are whole numbers of
   const bool copy = x != y && c.d > 2 * h->pairs;
   const int part = a.interleaved ? 2 * h->pairs : h->pairs, behind = copy ? c.d - 2 * h->pairs : 0;
@@ -317,16 +356,16 @@ extern "C" int ttt_rope_apply(const ttt_rope* h, int32_t B, int32_t H, int64_t N
   if (e == 2) {
     using T = __nv_bfloat16;
     if (one)
-      return wide == 16 ? launch<T, 16, true>(a, h->tab, copy, st)
-             : wide == 8 ? launch<T, 8, true>(a, h->tab, copy, st)
-                         : launch<T, 4, true>(a, h->tab, copy, st);
-    return wide == 16 ? launch<T, 16, false>(a, h->tab, copy, st)
-           : wide == 8 ? launch<T, 8, false>(a, h->tab, copy, st)
-           : wide == 4 ? launch<T, 4, false>(a, h->tab, copy, st)
-                       : launch<T, 2, false>(a, h->tab, copy, st);
+      return wide == 16 ? launch_heads<T, 16, true>(a, h->tab, copy, st)
+             : wide == 8 ? launch_heads<T, 8, true>(a, h->tab, copy, st)
+                         : launch_heads<T, 4, true>(a, h->tab, copy, st);
+    return wide == 16 ? launch_heads<T, 16, false>(a, h->tab, copy, st)
+           : wide == 8 ? launch_heads<T, 8, false>(a, h->tab, copy, st)
+           : wide == 4 ? launch_heads<T, 4, false>(a, h->tab, copy, st)
+                       : launch_heads<T, 2, false>(a, h->tab, copy, st);
   }
-  if (one) return wide == 16 ? launch<float, 16, true>(a, h->tab, copy, st) : launch<float, 8, true>(a, h->tab, copy, st);
-  return wide == 16 ? launch<float, 16, false>(a, h->tab, copy, st)
-         : wide == 8 ? launch<float, 8, false>(a, h->tab, copy, st)
-                     : launch<float, 4, false>(a, h->tab, copy, st);
+  if (one) return wide == 16 ? launch_heads<float, 16, true>(a, h->tab, copy, st) : launch_heads<float, 8, true>(a, h->tab, copy, st);
+  return wide == 16 ? launch_heads<float, 16, false>(a, h->tab, copy, st)
+         : wide == 8 ? launch_heads<float, 8, false>(a, h->tab, copy, st)
+                     : launch_heads<float, 4, false>(a, h->tab, copy, st);
 }
