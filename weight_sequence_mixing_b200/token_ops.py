@@ -17,12 +17,15 @@ synchronise and do not take part in autograd: `backward` is called with the grad
 from __future__ import annotations
 
 import ctypes
-from contextlib import nullcontext
 from dataclasses import dataclass, field
 
 import torch
 
-from .binding import DTYPE, LIB, TTT_ERR_TIMEOUT, _check
+from .binding import DTYPE, LIB, TTT_ERR_CUDA, TTT_ERR_TIMEOUT, _check
+
+# what a call of a few microseconds can afford of torch: no stream or device objects
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 PAIRING = {"halves": 0, "interleaved": 1}
 GATE = {"value": 0, "sigmoid": 1, "exp": 2}
@@ -31,6 +34,7 @@ ACT = {"none": 0, "silu": 1, "gelu": 2}
 POS_DTYPE = {torch.int32: 0, torch.float32: 1}
 MAX_AXES = 4
 _STATUS_TIMEOUT = 2
+_SHORT_SCAN = 16  # tokens up to which a scan needs no workspace
 
 
 class RopeConfig(ctypes.Structure):
@@ -65,6 +69,11 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _plain(x, shape, dtype):
+    """A new contiguous tensor on x's device."""
+    return x.new_empty(shape, dtype=dtype)
+
+
 @dataclass
 class _Op:
     """A configured operator: a C handle (host side only) bound to one device."""
@@ -80,14 +89,14 @@ class _Op:
     def _open(self, create, destroy, config):
         h = ctypes.c_void_p()
         _check(create(ctypes.byref(config), ctypes.byref(h)), create.__name__)
-        self._handle = h
-        self._destroy = destroy
+        self._handle, self._destroy = h, destroy
         self.io_dtype = torch.float32 if self.cfg["dtype"] == "f32" else torch.bfloat16
         dev = torch.device(self.device)
         if dev.type != "cuda":
             raise ValueError(f"device: expected a CUDA device, got {self.device}")
-        self._index = dev.index if dev.index is not None or not torch.cuda.is_available() else \
-            torch.cuda.current_device()
+        self._index = dev.index
+        if self._index is None:
+            self._index = torch.cuda.current_device() if torch.cuda.is_available() else 0
 
     def close(self):
         if self._handle:
@@ -100,36 +109,41 @@ class _Op:
         except Exception:
             pass
 
-    def _need_open(self):
+    def _open_handle(self):
         if not self._handle:
             raise ValueError(f"{type(self).__name__} is closed")
+        return self._handle
 
-    def _tensor(self, name, t, shape, dtype, rows=True):
-        """`t` is on this device, with this shape and dtype; its rows (rows=True) or all of it contiguous."""
+    def _rows(self, name, t, shape, dtype):
+        """`t` is on this device, of this shape and type, and its rows are contiguous."""
         if t.dtype != dtype or t.shape != shape:
             raise ValueError(f"{name}: expected shape {tuple(shape)} of {dtype}, got {tuple(t.shape)} of {t.dtype}")
-        if not t.is_cuda or t.device.index != self._index:
+        if t.get_device() != self._index:
             raise ValueError(f"{name}: expected a tensor on cuda:{self._index}, got one on {t.device}")
-        if rows:
-            if t.stride(-1) != 1 and t.shape[-1] > 1:
-                raise ValueError(f"{name}: the channels of a row must be contiguous, got strides {t.stride()}")
-        elif not t.is_contiguous():
-            raise ValueError(f"{name}: must be contiguous")
+        if t.stride(-1) != 1 and shape[-1] > 1:
+            raise ValueError(f"{name}: the channels of a row must be contiguous, got strides {t.stride()}")
 
-    def _on(self, stream, *tensors):
-        """The context to allocate and launch in.  Tensors handed to another stream than the
-        current one are kept from reuse until that stream is done with them."""
+    def _whole(self, name, t, shape, dtype):
+        """`t` is on this device, of this shape and type, and contiguous."""
+        self._rows(name, t, shape, dtype)
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous, got strides {t.stride()}")
+
+    def _run(self, stream, tensors, call, *args):
+        """call(*args) with this device current, on `stream` or the current stream.  Tensors handed to
+        another stream than the current one are kept from reuse until that stream is done with them."""
         if stream is None:
-            return nullcontext() if torch.cuda.current_device() == self._index else torch.cuda.device(self._index)
+            if _current_device() == self._index:
+                return call(*args)
+            with torch.cuda.device(self._index):
+                return call(*args)
         if stream.device.index != self._index:
             raise ValueError(f"stream: expected one of cuda:{self._index}, got one of {stream.device}")
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
-        return torch.cuda.stream(stream)
-
-    def _stream(self):
-        return torch.cuda.current_stream(self._index).cuda_stream
+        with torch.cuda.stream(stream):
+            return call(*args)
 
 
 class _StatusOp(_Op):
@@ -138,15 +152,20 @@ class _StatusOp(_Op):
     def _open(self, create, destroy, config):
         super()._open(create, destroy, config)
         self._status = torch.zeros(1, dtype=torch.int32, device=f"cuda:{self._index}")
+        self._status_ptr = self._status.data_ptr()
+
+    def _bytes(self, n):
+        """n bytes of workspace, or none."""
+        return torch.empty(n, dtype=torch.uint8, device=self._status.device) if n else None
 
     def check_status(self):
         """Waits for the device's work and raises if a call since the last check went wrong on the
-        device (a bounded wait ran out; the call's outputs hold NaN where they are unknown)."""
+        device (a bounded wait ran out; that call's outputs are not to be used)."""
         torch.cuda.synchronize(self._index)
         bits = int(self._status.item())
         if bits:
             self._status.zero_()
-            _check(TTT_ERR_TIMEOUT if bits & _STATUS_TIMEOUT else -3, "device status")
+            _check(TTT_ERR_TIMEOUT if bits & _STATUS_TIMEOUT else TTT_ERR_CUDA, "device status")
 
 
 class RotaryPositions(_Op):
@@ -167,40 +186,47 @@ class RotaryPositions(_Op):
         for i, (n, b) in enumerate(zip(pairs, base)):
             k.pairs[i], k.base[i] = n, b
         k.pairing, k.dtype = PAIRING[c.get("pairing", "halves")], DTYPE[c["dtype"]]
-        self.axes = len(pairs)
+        self.d, self.axes = int(c["d"]), len(pairs)
         self._open(LIB.ttt_rope_create, LIB.ttt_rope_destroy, k)
 
-    def _apply(self, x, pos, out, inverse, stream, name):
-        self._need_open()
-        if x.dim() != 4:
-            raise ValueError(f"{name}: expected [B, H, N, {self.cfg['d']}], got shape {tuple(x.shape)}")
-        B, H, N, _ = shape = x.shape
-        self._tensor(name, x, (B, H, N, self.cfg["d"]), self.io_dtype)
-        if pos.dtype not in POS_DTYPE or pos.shape not in ((N, self.axes), (B, N, self.axes)):
+    def _apply(self, name, x, pos, out, stream, inverse):
+        shape = x.shape
+        if len(shape) != 4:
+            raise ValueError(f"{name}: expected [B, H, N, {self.d}], got shape {tuple(shape)}")
+        B, H, N, _ = shape
+        self._rows(name, x, (B, H, N, self.d), self.io_dtype)
+        kind = POS_DTYPE.get(pos.dtype)
+        each = len(pos.shape) == 3
+        if kind is None or pos.shape != ((B, N, self.axes) if each else (N, self.axes)):
             raise ValueError(f"pos: expected [{N}, {self.axes}] or [{B}, {N}, {self.axes}] of int32 or float32, got "
                              f"shape {tuple(pos.shape)} of {pos.dtype}")
-        self._tensor("pos", pos, pos.shape, pos.dtype, rows=False)
-        with self._on(stream, x, pos, out):
-            if out is None:
-                out = torch.empty(shape, dtype=self.io_dtype, device=x.device)
-            else:
-                self._tensor("out", out, shape, self.io_dtype)
-            if x.numel():
-                xs, ys = x.stride(), out.stride()
-                _check(LIB.ttt_rope_apply(self._handle, B, H, N, x.data_ptr(), _strides(xs[0], xs[1], xs[2]),
-                                          pos.data_ptr(), POS_DTYPE[pos.dtype], N * self.axes if pos.dim() == 3 else 0,
-                                          out.data_ptr(), _strides(ys[0], ys[1], ys[2]), inverse, self._stream()),
-                       "ttt_rope_apply")
+        self._whole("pos", pos, pos.shape, pos.dtype)
+        if out is not None:
+            self._rows("out", out, shape, self.io_dtype)
+        return self._run(stream, (x, pos, out), self._launch, self._open_handle(), x, pos, out, kind, each, inverse)
+
+    def _launch(self, handle, x, pos, out, kind, each, inverse):
+        shape = x.shape
+        if out is None:
+            out = _plain(x, shape, self.io_dtype)
+        B, H, N, _ = shape
+        if B and H and N:
+            xs, ys = x.stride(), out.stride()
+            st = LIB.ttt_rope_apply(handle, B, H, N, x.data_ptr(), _strides(xs[0], xs[1], xs[2]), pos.data_ptr(), kind,
+                                    N * self.axes if each else 0, out.data_ptr(), _strides(ys[0], ys[1], ys[2]),
+                                    inverse, _current_stream(self._index))
+            if st:
+                _check(st, "ttt_rope_apply")
         return out
 
     def forward(self, x, pos, out=None, stream=None):
         """x [B, H, N, d] (any strides, channels contiguous) turned to its positions pos [N, axes] or
         [B, N, axes], int32 or float32.  out: given, and then possibly x itself, or a new contiguous tensor."""
-        return self._apply(x, pos, out, 0, stream, "x")
+        return self._apply("x", x, pos, out, stream, 0)
 
     def backward(self, dy, pos, out=None, stream=None):
         """The gradient of forward with respect to x: the rotation the other way."""
-        return self._apply(dy, pos, out, 1, stream, "dy")
+        return self._apply("dy", dy, pos, out, stream, 1)
 
 
 class GatedScan(_StatusOp):
@@ -216,85 +242,93 @@ class GatedScan(_StatusOp):
         self.D = int(c["D"])
         self._open(LIB.ttt_scan_create, LIB.ttt_scan_destroy, k)
 
-    def _rows(self, B, L, **tensors):
-        for name, t in tensors.items():
-            if t is not None:
-                self._tensor(name, t, (B, L, self.D), self.io_dtype)
-
-    def _state(self, B, lengths, **tensors):
-        for name, t in tensors.items():
-            if t is not None:
-                self._tensor(name, t, (B, self.D), torch.float32, rows=False)
+    def _sizes(self, x, lengths):
+        shape = x.shape
+        if len(shape) != 3 or shape[0] < 1:
+            raise ValueError(f"x: expected [B, L, {self.D}], got shape {tuple(shape)}")
         if lengths is not None:
-            self._tensor("lengths", lengths, (B,), torch.int32, rows=False)
+            self._whole("lengths", lengths, (shape[0],), torch.int32)
+        return (shape[0], shape[1], self.D), (shape[0], self.D)
 
-    def _shape(self, t, name):
-        self._need_open()
-        if t.dim() != 3 or t.shape[0] < 1:
-            raise ValueError(f"{name}: expected [B, L, {self.D}], got shape {tuple(t.shape)}")
-        return t.shape[0], t.shape[1]
+    def _saved_bytes(self, B, L):
+        return LIB.ttt_scan_saved_size(self._open_handle(), B, L)
 
-    def _new(self, B, L, lengths, like):
-        # rows behind a sequence's end are left as they are: zeros, in a tensor made here
-        make = torch.empty if lengths is None else torch.zeros
-        return make((B, L, self.D), dtype=self.io_dtype, device=like.device)
-
-    def _workspace(self, B, L, like):
-        n = LIB.ttt_scan_workspace_size(self._handle, B, L)
-        return (torch.empty(n, dtype=torch.uint8, device=like.device), n) if n else (None, 0)
+    def _check_saved(self, saved, B, L):
+        n = self._saved_bytes(B, L)
+        if saved.dtype != torch.uint8 or saved.numel() < n or not saved.is_contiguous() or \
+                saved.get_device() != self._index:
+            raise ValueError(f"saved: expected at least {n} contiguous bytes on cuda:{self._index} (new_saved)")
 
     def new_saved(self, B: int, L: int, stream=None):
         """A buffer for what a forward call leaves for its backward call."""
-        self._need_open()
-        with self._on(stream):
-            return torch.empty(max(16, LIB.ttt_scan_saved_size(self._handle, B, L)), dtype=torch.uint8,
-                               device=f"cuda:{self._index}")
+        return self._run(stream, (), self._bytes, max(16, self._saved_bytes(B, L)))
 
-    def _check_saved(self, saved, B, L):
-        n = LIB.ttt_scan_saved_size(self._handle, B, L)
-        if saved.dtype != torch.uint8 or saved.numel() < n or not saved.is_contiguous() or \
-                saved.device.index != self._index:
-            raise ValueError(f"saved: expected at least {n} contiguous bytes on cuda:{self._index} (new_saved)")
+    def _new(self, x, shape, lengths):
+        # rows behind a sequence's end are left as they are: zeros, in a tensor made here
+        return _plain(x, shape, self.io_dtype) if lengths is None else x.new_zeros(shape, dtype=self.io_dtype)
 
     def forward(self, g, x, h0=None, lengths=None, saved=None, out=None, h_last=None, stream=None):
         """Returns (h [B, L, D], h_last [B, D]).  lengths: [B] int32, each sequence's own length; rows from
-        there on are not read and are left as they were in `out` (zero where it is not given).  h_last may be h0."""
-        B, L = self._shape(x, "x")
-        self._rows(B, L, g=g, x=x, out=out)
-        self._state(B, lengths, h0=h0, h_last=h_last)
+        there on are not used and are left as they were in `out` (zero where it is not given).  h_last may be h0."""
+        shape, state = self._sizes(x, lengths)
+        self._rows("x", x, shape, self.io_dtype)
+        self._rows("g", g, shape, self.io_dtype)
+        if out is not None:
+            self._rows("out", out, shape, self.io_dtype)
+        if h0 is not None:
+            self._whole("h0", h0, state, torch.float32)
+        if h_last is not None:
+            self._whole("h_last", h_last, state, torch.float32)
         if saved is not None:
-            self._check_saved(saved, B, L)
-        with self._on(stream, g, x, h0, lengths, saved, out, h_last):
-            if out is None:
-                out = self._new(B, L, lengths, x)
-            if h_last is None:
-                h_last = torch.empty((B, self.D), dtype=torch.float32, device=x.device)
-            ws, n = self._workspace(B, L, x)
-            gs, xs, hs = g.stride(), x.stride(), out.stride()
-            _check(LIB.ttt_scan_forward(self._handle, B, L, g.data_ptr(), _strides(gs[0], 0, gs[1]), x.data_ptr(),
-                                        _strides(xs[0], 0, xs[1]), _ptr(h0), _ptr(lengths), out.data_ptr(),
-                                        _strides(hs[0], 0, hs[1]), h_last.data_ptr(), _ptr(saved), _ptr(ws), n,
-                                        self._status.data_ptr(), self._stream()), "ttt_scan_forward")
+            self._check_saved(saved, shape[0], shape[1])
+        return self._run(stream, (g, x, h0, lengths, saved, out, h_last), self._launch_forward, self._open_handle(), g, x,
+                         h0, lengths, saved, out, h_last, shape, state)
+
+    def _launch_forward(self, handle, g, x, h0, lengths, saved, out, h_last, shape, state):
+        B, L, _ = shape
+        if out is None:
+            out = self._new(x, shape, lengths)
+        if h_last is None:
+            h_last = _plain(x, state, torch.float32)
+        n = LIB.ttt_scan_workspace_size(handle, B, L) if L > _SHORT_SCAN else 0
+        ws = self._bytes(n)
+        gs, xs, hs = g.stride(), x.stride(), out.stride()
+        st = LIB.ttt_scan_forward(handle, B, L, g.data_ptr(), _strides(gs[0], 0, gs[1]), x.data_ptr(),
+                                  _strides(xs[0], 0, xs[1]), _ptr(h0), _ptr(lengths), out.data_ptr(),
+                                  _strides(hs[0], 0, hs[1]), h_last.data_ptr(), _ptr(saved), _ptr(ws), n,
+                                  self._status_ptr, _current_stream(self._index))
+        if st:
+            _check(st, "ttt_scan_forward")
         return out, h_last
 
     def backward(self, dh, g, x, saved, dh_last=None, lengths=None, dg=None, dx=None, dh0=None, stream=None):
         """Gradients (dg, dx [B, L, D], dh0 [B, D]) of a forward call with the same g, x and lengths that was
         given `saved`.  Rows behind a sequence's end are left as they were (zero in tensors made here)."""
-        B, L = self._shape(x, "x")
-        self._rows(B, L, dh=dh, g=g, x=x, dg=dg, dx=dx)
-        self._state(B, lengths, dh_last=dh_last, dh0=dh0)
-        self._check_saved(saved, B, L)
-        with self._on(stream, dh, g, x, saved, dh_last, lengths, dg, dx, dh0):
-            dg = self._new(B, L, lengths, x) if dg is None else dg
-            dx = self._new(B, L, lengths, x) if dx is None else dx
-            if dh0 is None:
-                dh0 = torch.empty((B, self.D), dtype=torch.float32, device=x.device)
-            ws, n = self._workspace(B, L, x)
-            s = [_strides(t.stride(0), 0, t.stride(1)) for t in (dh, g, x, dg, dx)]
-            _check(LIB.ttt_scan_backward(self._handle, B, L, dh.data_ptr(), s[0], _ptr(dh_last), g.data_ptr(), s[1],
-                                         x.data_ptr(), s[2], _ptr(lengths), saved.data_ptr(), dg.data_ptr(), s[3],
-                                         dx.data_ptr(), s[4], dh0.data_ptr(), _ptr(ws), n, self._status.data_ptr(),
-                                         self._stream()), "ttt_scan_backward")
+        shape, state = self._sizes(x, lengths)
+        for name, t in (("x", x), ("g", g), ("dh", dh), ("dg", dg), ("dx", dx)):
+            if t is not None:
+                self._rows(name, t, shape, self.io_dtype)
+        for name, t in (("dh_last", dh_last), ("dh0", dh0)):
+            if t is not None:
+                self._whole(name, t, state, torch.float32)
+        self._check_saved(saved, shape[0], shape[1])
+        return self._run(stream, (dh, g, x, saved, dh_last, lengths, dg, dx, dh0), self._launch_backward,
+                         self._open_handle(), dh, g, x, saved, dh_last, lengths, dg, dx, dh0, shape, state)
+
+    def _launch_backward(self, handle, dh, g, x, saved, dh_last, lengths, dg, dx, dh0, shape, state):
+        B, L, _ = shape
+        dg = self._new(x, shape, lengths) if dg is None else dg
+        dx = self._new(x, shape, lengths) if dx is None else dx
+        if dh0 is None:
+            dh0 = _plain(x, state, torch.float32)
+        n = LIB.ttt_scan_workspace_size(handle, B, L) if L > _SHORT_SCAN else 0
+        ws = self._bytes(n)
+        s = [_strides(t.stride(0), 0, t.stride(1)) for t in (dh, g, x, dg, dx)]
+        st = LIB.ttt_scan_backward(handle, B, L, dh.data_ptr(), s[0], _ptr(dh_last), g.data_ptr(), s[1], x.data_ptr(),
+                                   s[2], _ptr(lengths), saved.data_ptr(), dg.data_ptr(), s[3], dx.data_ptr(), s[4],
+                                   dh0.data_ptr(), _ptr(ws), n, self._status_ptr, _current_stream(self._index))
+        if st:
+            _check(st, "ttt_scan_backward")
         return dg, dx, dh0
 
 
@@ -309,78 +343,87 @@ class GroupNorm(_StatusOp):
         c, k = self.cfg, NormConfig()
         k.C, k.groups, k.act, k.eps = c["C"], c["groups"], ACT[c.get("act", "none")], c.get("eps", 1e-5)
         k.dtype = DTYPE[c["dtype"]]
-        self.C, self.groups = int(c["C"]), int(c["groups"])
         self._open(LIB.ttt_norm_create, LIB.ttt_norm_destroy, k)
+        self.C, self.groups = int(c["C"]), int(c["groups"])
+        self._each = self.C // self.groups  # channels of a group
 
     def new_stats(self, B: int, stream=None):
         """A buffer for the mean and 1 / sqrt(var + eps) of every group, for the backward call."""
-        self._need_open()
-        with self._on(stream):
-            return torch.empty((B, self.groups, 2), dtype=torch.float32, device=f"cuda:{self._index}")
+        self._open_handle()
+        return self._run(stream, (), lambda: torch.empty((B, self.groups, 2), dtype=torch.float32,
+                                                         device=self._status.device))
 
-    def _shape(self, x):
-        self._need_open()
-        n = self.C // self.groups
-        if x.dim() == 4 and x.shape == (x.shape[0], self.groups, x.shape[2], n):
-            B, N, shape = x.shape[0], x.shape[2], x.shape
-        elif x.dim() == 3:
-            B, N, shape = x.shape[0], x.shape[1], (x.shape[0], x.shape[1], self.C)
+    def _shapes(self, x):
+        """(shape x has to have, [B, N, C])"""
+        s = x.shape
+        if len(s) == 3:
+            want = rows = (s[0], s[1], self.C)
+        elif len(s) == 4:
+            want, rows = (s[0], self.groups, s[2], self._each), (s[0], s[2], self.C)
         else:
-            raise ValueError(f"x: expected [B, N, {self.C}] or [B, {self.groups}, N, {n}], got {tuple(x.shape)}")
-        if B < 1 or N < 1:
-            raise ValueError(f"x: no statistics of an empty tensor, got shape {tuple(x.shape)}")
-        return B, N, shape
+            raise ValueError(f"x: expected [B, N, {self.C}] or [B, {self.groups}, N, {self._each}], got {tuple(s)}")
+        if s[0] < 1 or rows[1] < 1:
+            raise ValueError(f"x: no statistics of an empty tensor, got shape {tuple(s)}")
+        return want, rows
 
     def _strides(self, t):
         s = t.stride()
-        return _strides(s[0], self.C // self.groups, s[1]) if t.dim() == 3 else _strides(s[0], s[1], s[2])
-
-    def _workspace(self, B, N, backward, like):
-        n = LIB.ttt_norm_workspace_size(self._handle, B, N, backward)
-        return (torch.empty(n, dtype=torch.uint8, device=like.device), n) if n else (None, 0)
-
-    def _weights(self, **tensors):
-        for name, t in tensors.items():
-            if t is not None:
-                self._tensor(name, t, (self.C,), torch.float32, rows=False)
+        return _strides(s[0], self._each, s[1]) if len(s) == 3 else _strides(s[0], s[1], s[2])
 
     def forward(self, x, weight=None, bias=None, stats=None, out=None, stream=None):
         """y [B, N, C].  weight, bias: [C] fp32.  out: given, and then possibly x itself, or new."""
-        B, N, shape = self._shape(x)
-        self._tensor("x", x, shape, self.io_dtype)
-        self._weights(weight=weight, bias=bias)
+        want, rows = self._shapes(x)
+        self._rows("x", x, want, self.io_dtype)
+        if weight is not None:
+            self._whole("weight", weight, (self.C,), torch.float32)
+        if bias is not None:
+            self._whole("bias", bias, (self.C,), torch.float32)
         if stats is not None:
-            self._tensor("stats", stats, (B, self.groups, 2), torch.float32, rows=False)
+            self._whole("stats", stats, (rows[0], self.groups, 2), torch.float32)
         if out is not None:
-            self._tensor("out", out, (B, N, self.C), self.io_dtype)
-        with self._on(stream, x, weight, bias, stats, out):
-            if out is None:
-                out = torch.empty((B, N, self.C), dtype=self.io_dtype, device=x.device)
-            ws, n = self._workspace(B, N, 0, x)
-            _check(LIB.ttt_norm_forward(self._handle, B, N, x.data_ptr(), self._strides(x), _ptr(weight), _ptr(bias),
-                                        out.data_ptr(), self._strides(out), _ptr(stats), _ptr(ws), n,
-                                        self._status.data_ptr(), self._stream()), "ttt_norm_forward")
+            self._rows("out", out, rows, self.io_dtype)
+        return self._run(stream, (x, weight, bias, stats, out), self._launch_forward, self._open_handle(), x, weight, bias,
+                         stats, out, rows)
+
+    def _launch_forward(self, handle, x, weight, bias, stats, out, rows):
+        if out is None:
+            out = _plain(x, rows, self.io_dtype)
+        n = LIB.ttt_norm_workspace_size(handle, rows[0], rows[1], 0)
+        ws = self._bytes(n)
+        st = LIB.ttt_norm_forward(handle, rows[0], rows[1], x.data_ptr(), self._strides(x), _ptr(weight), _ptr(bias),
+                                  out.data_ptr(), self._strides(out), _ptr(stats), _ptr(ws), n, self._status_ptr,
+                                  _current_stream(self._index))
+        if st:
+            _check(st, "ttt_norm_forward")
         return out
 
     def backward(self, dy, x, weight, bias, stats, dx=None, dweight=None, dbias=None, stream=None):
         """Gradients (dx of x's shape, dweight [C], dbias [C]) of a forward call that was given `stats`."""
-        B, N, shape = self._shape(x)
-        self._tensor("x", x, shape, self.io_dtype)
-        self._tensor("dy", dy, (B, N, self.C), self.io_dtype)
-        self._weights(weight=weight, bias=bias, dweight=dweight, dbias=dbias)
-        self._tensor("stats", stats, (B, self.groups, 2), torch.float32, rows=False)
+        want, rows = self._shapes(x)
+        self._rows("x", x, want, self.io_dtype)
+        self._rows("dy", dy, rows, self.io_dtype)
+        for name, t in (("weight", weight), ("bias", bias), ("dweight", dweight), ("dbias", dbias)):
+            if t is not None:
+                self._whole(name, t, (self.C,), torch.float32)
+        self._whole("stats", stats, (rows[0], self.groups, 2), torch.float32)
         if dx is not None:
-            self._tensor("dx", dx, shape, self.io_dtype)
-        with self._on(stream, dy, x, weight, bias, stats, dx, dweight, dbias):
-            if dx is None:
-                dx = torch.empty(shape, dtype=self.io_dtype, device=x.device)
-            if dweight is None:
-                dweight = torch.empty(self.C, dtype=torch.float32, device=x.device)
-            if dbias is None:
-                dbias = torch.empty(self.C, dtype=torch.float32, device=x.device)
-            ws, n = self._workspace(B, N, 1, x)
-            _check(LIB.ttt_norm_backward(self._handle, B, N, dy.data_ptr(), self._strides(dy), x.data_ptr(),
-                                         self._strides(x), _ptr(weight), _ptr(bias), stats.data_ptr(), dx.data_ptr(),
-                                         self._strides(dx), dweight.data_ptr(), dbias.data_ptr(), _ptr(ws), n,
-                                         self._status.data_ptr(), self._stream()), "ttt_norm_backward")
+            self._rows("dx", dx, want, self.io_dtype)
+        return self._run(stream, (dy, x, weight, bias, stats, dx, dweight, dbias), self._launch_backward,
+                         self._open_handle(), dy, x, weight, bias, stats, dx, dweight, dbias, want, rows)
+
+    def _launch_backward(self, handle, dy, x, weight, bias, stats, dx, dweight, dbias, want, rows):
+        if dx is None:
+            dx = _plain(x, want, self.io_dtype)
+        if dweight is None:
+            dweight = _plain(x, (self.C,), torch.float32)
+        if dbias is None:
+            dbias = _plain(x, (self.C,), torch.float32)
+        n = LIB.ttt_norm_workspace_size(handle, rows[0], rows[1], 1)
+        ws = self._bytes(n)
+        st = LIB.ttt_norm_backward(handle, rows[0], rows[1], dy.data_ptr(), self._strides(dy), x.data_ptr(),
+                                   self._strides(x), _ptr(weight), _ptr(bias), stats.data_ptr(), dx.data_ptr(),
+                                   self._strides(dx), dweight.data_ptr(), dbias.data_ptr(), _ptr(ws), n,
+                                   self._status_ptr, _current_stream(self._index))
+        if st:
+            _check(st, "ttt_norm_backward")
         return dx, dweight, dbias
