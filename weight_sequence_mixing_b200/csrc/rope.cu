@@ -6,15 +6,13 @@
 // 64-bit fraction, the low 64 bits of the product are the turn.  For an fp32 p the product
 // and its reduction are in fp64.  (In 32 bits the product is off by p 2^-24 turns: a
 // position of 10^6 would lose three digits of the angle.)
-#include <cuda_bf16.h>
-#include <cuda_runtime.h>
-
 #include <algorithm>
 #include <cmath>
 #include <new>
 
 #include "op_checks.h"
 #include "ttt_plan.cuh"
+#include "vec.cuh"
 
 namespace ttt {
 namespace {
@@ -41,84 +39,6 @@ struct RopeArgs {
   int32_t item_blocks, head_groups;
   int64_t tiles;                // of tokens, times head groups and batch entries
   int64_t row_tiles;            // of tokens
-};
-
-template <class T>
-__device__ __forceinline__ void open_word(uint32_t w, float (&v)[4 / sizeof(T)]) {
-  if constexpr (sizeof(T) == 4) {
-    v[0] = __uint_as_float(w);
-  } else {
-    v[0] = __uint_as_float(w << 16);
-    v[1] = __uint_as_float(w & 0xffff0000u);
-  }
-}
-template <class T>
-__device__ __forceinline__ uint32_t close_word(const float (&v)[4 / sizeof(T)]) {
-  if constexpr (sizeof(T) == 4) {
-    return __float_as_uint(v[0]);
-  } else {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(v[0], v[1]);
-    return *reinterpret_cast<const uint32_t*>(&p);
-  }
-}
-
-// BYTES of consecutive channels
-template <class T, int BYTES>
-struct Vec {
-  static constexpr int N = BYTES / sizeof(T);
-  static constexpr int kWords = (BYTES + 3) / 4;
-  uint32_t w[kWords];
-  __device__ __forceinline__ void load(const T* p) {
-    if constexpr (BYTES == 16) {
-      const uint4 q = *reinterpret_cast<const uint4*>(p);
-      w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
-    } else if constexpr (BYTES == 8) {
-      const uint2 q = *reinterpret_cast<const uint2*>(p);
-      w[0] = q.x, w[1] = q.y;
-    } else if constexpr (BYTES == 4) {
-      w[0] = *reinterpret_cast<const uint32_t*>(p);
-    } else {
-      w[0] = *reinterpret_cast<const uint16_t*>(p);
-    }
-  }
-  __device__ __forceinline__ void store(T* p) const {
-    if constexpr (BYTES == 16)
-      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    else if constexpr (BYTES == 8)
-      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-    else if constexpr (BYTES == 4)
-      *reinterpret_cast<uint32_t*>(p) = w[0];
-    else
-      *reinterpret_cast<uint16_t*>(p) = uint16_t(w[0]);
-  }
-  __device__ __forceinline__ void open(float (&v)[N]) const {
-    if constexpr (BYTES == 2) {
-      v[0] = __uint_as_float(w[0] << 16);
-    } else {
-      constexpr int K = 4 / sizeof(T);
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) {
-        float u[K];
-        open_word<T>(w[i], u);
-#pragma unroll
-        for (int k = 0; k < K; ++k) v[i * K + k] = u[k];
-      }
-    }
-  }
-  __device__ __forceinline__ void close(const float (&v)[N]) {
-    if constexpr (BYTES == 2) {
-      w[0] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
-    } else {
-      constexpr int K = 4 / sizeof(T);
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) {
-        float u[K];
-#pragma unroll
-        for (int k = 0; k < K; ++k) u[k] = v[i * K + k];
-        w[i] = close_word<T>(u);
-      }
-    }
-  }
 };
 
 // A thread owns a vector of pairs (or of channels that are only copied) of every token: its
