@@ -68,12 +68,19 @@ __device__ __forceinline__ float2 finish(const Part& v, float eps) {  // mean, 1
   return make_float2(v.mean, 1.f / sqrtf(v.S / v.n + eps));
 }
 
-// sigma(z).  bf16 outputs take the hardware's exponential and reciprocal (2^-22 off), fp32
-// ones the library's.
+// sigma(z).  bf16 outputs take the hardware's exponential (2^-22 off, and 2^-24 of the
+// exponent's size), fp32 ones the library's; the reciprocal is the hardware's, 2^-23 off.
+__device__ __forceinline__ float rcp_fast(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
 template <class T>
 __device__ __forceinline__ float sigmoid(float z) {
-  if (sizeof(T) == 2) return __fdividef(1.f, 1.f + __expf(-z));
-  return 1.f / (1.f + expf(-z));
+  if (sizeof(T) == 4) return rcp_fast(1.f + expf(-z));
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+  return rcp_fast(1.f + e);
 }
 constexpr float kInvSqrt2 = 0.70710678118654752f, kInvSqrt2Pi = 0.39894228040143268f;
 template <class T, int ACT>
@@ -113,12 +120,12 @@ __device__ __forceinline__ int block_end(const NormArgs& p, int col_block, int V
 }
 
 // Statistics of one range of tokens and block of channels: a thread walks down its channels,
-// a warp then joins the threads' parts of each group.
-template <class T, int BYTES>
-__global__ void __launch_bounds__(kThreads) norm_parts_kernel(const __grid_constant__ NormArgs p) {
+// Q of them (all of one group) to a sum; a warp then joins the threads' parts of each group.
+template <class T, int BYTES, int Q>
+__global__ void __launch_bounds__(kThreads, 3) norm_parts_kernel(const __grid_constant__ NormArgs p) {
   using X = Vec<T, BYTES>;
-  constexpr int V = X::N, kAtOnce = 4;
-  extern __shared__ float2 threads[];  // [row][channel of the block]
+  constexpr int V = X::N, K = V / Q, kAtOnce = 8;
+  extern __shared__ float2 threads[];  // [row][sum of the block]
   const int cb = blockIdx.x, rb = blockIdx.y, b = blockIdx.z;
   const Column k = column(p, cb, V);
   const int row = threadIdx.x / p.lanes;
@@ -127,36 +134,39 @@ __global__ void __launch_bounds__(kThreads) norm_parts_kernel(const __grid_const
   if (k.here) {
     const T* x = static_cast<const T*>(p.x) + k.at(p.xs, b) + (t0 + row) * p.xs[2];
     const int64_t hop = p.rows * p.xs[2];
-    float count = 0.f, mean[V] = {}, S[V] = {};
+    float count = 0.f, mean[K] = {}, S[K] = {};
     for (int64_t left = tokens > row ? (tokens - row + p.rows - 1) / p.rows : 0; left > 0;) {
       const int run = left < kRun ? int(left) : kRun;
-      float first[V], s[V], q[V];
-      X v[kAtOnce];
+      float first[K], s[K], q[K];
       for (int j = 0; j < run; j += kAtOnce) {
+        X v[kAtOnce];
 #pragma unroll
-        for (int e = 0; e < kAtOnce; ++e)
-          if (j + e < run) v[e].load(x + e * hop);
-        x += min(kAtOnce, run - j) * hop;
+        for (int e = 0; e < kAtOnce; ++e) {
+          if (j + e < run) v[e].load(x);
+          x += j + e < run ? hop : 0;
+        }
+        if (j == 0) {
+          float f[V];
+          v[0].open(f);
+#pragma unroll
+          for (int i = 0; i < K; ++i) first[i] = f[i * Q], s[i] = 0.f, q[i] = 0.f;
+        }
 #pragma unroll
         for (int e = 0; e < kAtOnce; ++e)
           if (j + e < run) {
             float f[V];
             v[e].open(f);
-            if (j + e == 0) {
-#pragma unroll
-              for (int i = 0; i < V; ++i) first[i] = f[i], s[i] = 0.f, q[i] = 0.f;
-            }
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-              const float d = f[i] - first[i];
-              s[i] += d;
-              q[i] = fmaf(d, d, q[i]);
+              const float d = f[i] - first[i / Q];
+              s[i / Q] += d;
+              q[i / Q] = fmaf(d, d, q[i / Q]);
             }
           }
       }
-      const float n = float(run), inv = 1.f / n, all = count + n, f = n / all;
+      const float n = float(run * Q), inv = 1.f / n, all = count + n, f = n / all;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
+      for (int i = 0; i < K; ++i) {
         const float m = s[i] * inv, Si = fmaxf(fmaf(-s[i], m, q[i]), 0.f);
         const float d = first[i] + m - mean[i];
         if (count == 0.f) {
@@ -171,18 +181,19 @@ __global__ void __launch_bounds__(kThreads) norm_parts_kernel(const __grid_const
       left -= run;
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) threads[row * width + (threadIdx.x % p.lanes) * V + i] = make_float2(mean[i], S[i]);
+    for (int i = 0; i < K; ++i)
+      threads[(row * p.lanes + threadIdx.x % p.lanes) * K + i] = make_float2(mean[i], S[i]);
   }
   __syncthreads();
   const int c0 = cb * width, c1 = block_end(p, cb, V), g0 = c0 / p.n;
   const int lane = threadIdx.x % 32;
   for (int g = g0 + threadIdx.x / 32; g <= (c1 - 1) / p.n; g += kThreads / 32) {
-    const int from = max(g * p.n, c0), to = min((g + 1) * p.n, c1), wide = to - from;
+    const int from = (max(g * p.n, c0) - c0) / Q, wide = (min((g + 1) * p.n, c1) - c0) / Q - from;
     Part v = {0.f, 0.f, 0.f};
     for (int e = lane; e < p.rows * wide; e += 32) {
-      const int r = e / wide, c = from + e % wide - c0;
-      const float n = tokens > r ? float((tokens - r + p.rows - 1) / p.rows) : 0.f;
-      const float2 m = threads[r * width + c];
+      const int r = e / wide;
+      const float n = tokens > r ? float((tokens - r + p.rows - 1) / p.rows * Q) : 0.f;
+      const float2 m = threads[r * (p.lanes * K) + from + e % wide];
       v = join(v, {n, m.x, m.y});
     }
     v = join_warp(v);
@@ -208,10 +219,10 @@ __device__ __forceinline__ float2 join_parts(const NormArgs& p, int b, int g, in
 }
 
 // Joins the parts of its groups and normalises one range of tokens and block of channels.
-template <class T, int BYTES, int ACT>
-__global__ void __launch_bounds__(kThreads) norm_apply_kernel(const __grid_constant__ NormArgs p) {
+template <class T, int BYTES, int Q, int ACT>
+__global__ void __launch_bounds__(kThreads, 3) norm_apply_kernel(const __grid_constant__ NormArgs p) {
   using X = Vec<T, BYTES>;
-  constexpr int V = X::N, kAtOnce = 4;
+  constexpr int V = X::N, K = V / Q, kAtOnce = 8;
   extern __shared__ float2 known[];  // (mean, 1 / std) of the block's groups
   const int cb = gridDim.x - 1 - blockIdx.x, rb = gridDim.y - 1 - blockIdx.y, b = gridDim.z - 1 - blockIdx.z;
   const Column k = column(p, cb, V);
@@ -227,13 +238,16 @@ __global__ void __launch_bounds__(kThreads) norm_apply_kernel(const __grid_const
   }
   __syncthreads();
   if (!k.here) return;
-  float mean[V], scale[V], shift[V];
+  float mean[K], scale[V], shift[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const float2 m = known[(k.c + i) / p.n - g0];
-    mean[i] = m.x;
-    scale[i] = m.y * (p.weight ? p.weight[k.c + i] : 1.f);
-    shift[i] = p.bias ? p.bias[k.c + i] : 0.f;
+  for (int j = 0; j < K; ++j) {
+    const float2 m = known[(k.c + j * Q) / p.n - g0];
+    mean[j] = m.x;
+#pragma unroll
+    for (int i = j * Q; i < (j + 1) * Q; ++i) {
+      scale[i] = m.y * (p.weight ? p.weight[k.c + i] : 1.f);
+      shift[i] = p.bias ? p.bias[k.c + i] : 0.f;
+    }
   }
   const int64_t t0 = rb * p.range, tokens = min(p.range, p.N - t0);
   const T* x = static_cast<const T*>(p.x) + k.at(p.xs, b) + (t0 + row) * p.xs[2];
@@ -250,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) norm_apply_kernel(const __grid_const
         float f[V];
         v[e].open(f);
 #pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = act<T, ACT>(fmaf(f[i] - mean[i], scale[i], shift[i]));
+        for (int i = 0; i < V; ++i) f[i] = act<T, ACT>(fmaf(f[i] - mean[i / Q], scale[i], shift[i]));
         v[e].close(f);
         v[e].store(y + (j + e) * p.rows * p.ys[2]);
       }
@@ -258,10 +272,10 @@ __global__ void __launch_bounds__(kThreads) norm_apply_kernel(const __grid_const
 }
 
 // Backward, of one range of tokens and block of channels: each channel's sums of dz and dz xhat
-template <class T, int BYTES, int ACT>
-__global__ void __launch_bounds__(kThreads) norm_sums_kernel(const __grid_constant__ NormArgs p) {
+template <class T, int BYTES, int Q, int ACT>
+__global__ void __launch_bounds__(kThreads, 2) norm_sums_kernel(const __grid_constant__ NormArgs p) {
   using X = Vec<T, BYTES>;
-  constexpr int V = X::N, kAtOnce = 2;
+  constexpr int V = X::N, K = V / Q, kAtOnce = 4;
   extern __shared__ float2 threads[];
   const int cb = blockIdx.x, rb = blockIdx.y, b = blockIdx.z;
   const Column k = column(p, cb, V);
@@ -269,12 +283,15 @@ __global__ void __launch_bounds__(kThreads) norm_sums_kernel(const __grid_consta
   const int64_t t0 = rb * p.range, tokens = min(p.range, p.N - t0);
   const int width = p.lanes * V;
   if (k.here) {
-    float mean[V], rstd[V], w[V], o[V], total0[V] = {}, total1[V] = {};
+    float mean[K], rstd[K], w[V], o[V], total0[V] = {}, total1[V] = {};
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float2 m = reinterpret_cast<const float2*>(p.stats)[int64_t(b) * p.G + (k.c + i) / p.n];
+    for (int i = 0; i < K; ++i) {
+      const float2 m = reinterpret_cast<const float2*>(p.stats)[int64_t(b) * p.G + (k.c + i * Q) / p.n];
       mean[i] = m.x;
       rstd[i] = m.y;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
       w[i] = p.weight ? p.weight[k.c + i] : 1.f;
       o[i] = p.bias ? p.bias[k.c + i] : 0.f;
     }
@@ -287,13 +304,14 @@ __global__ void __launch_bounds__(kThreads) norm_sums_kernel(const __grid_consta
       for (int j = 0; j < run; j += kAtOnce) {
         X v[kAtOnce], d[kAtOnce];
 #pragma unroll
-        for (int e = 0; e < kAtOnce; ++e)
+        for (int e = 0; e < kAtOnce; ++e) {
           if (j + e < run) {
-            v[e].load(x + e * hop);
-            d[e].load(dy + e * dhop);
+            v[e].load(x);
+            d[e].load(dy);
           }
-        x += min(kAtOnce, run - j) * hop;
-        dy += min(kAtOnce, run - j) * dhop;
+          x += j + e < run ? hop : 0;
+          dy += j + e < run ? dhop : 0;
+        }
 #pragma unroll
         for (int e = 0; e < kAtOnce; ++e)
           if (j + e < run) {
@@ -302,7 +320,7 @@ __global__ void __launch_bounds__(kThreads) norm_sums_kernel(const __grid_consta
             d[e].open(g);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-              const float xhat = (f[i] - mean[i]) * rstd[i];
+              const float xhat = (f[i] - mean[i / Q]) * rstd[i / Q];
               const float dz = g[i] * act_grad<T, ACT>(fmaf(xhat, w[i], o[i]));
               s0[i] += dz;
               s1[i] = fmaf(dz, xhat, s1[i]);
@@ -363,10 +381,10 @@ __global__ void __launch_bounds__(1024) norm_join_sums_kernel(const __grid_const
 }
 
 // dx of one range of tokens and block of channels, walked backwards
-template <class T, int BYTES, int ACT>
-__global__ void __launch_bounds__(kThreads) norm_dx_kernel(const __grid_constant__ NormArgs p) {
+template <class T, int BYTES, int Q, int ACT>
+__global__ void __launch_bounds__(kThreads, 2) norm_dx_kernel(const __grid_constant__ NormArgs p) {
   using X = Vec<T, BYTES>;
-  constexpr int V = X::N, kAtOnce = 2;
+  constexpr int V = X::N, K = V / Q, kAtOnce = 4;
   extern __shared__ float2 known[];  // (mean q, mean q xhat) of the block's groups
   const int cb = gridDim.x - 1 - blockIdx.x, rb = gridDim.y - 1 - blockIdx.y, b = gridDim.z - 1 - blockIdx.z;
   const Column k = column(p, cb, V);
@@ -387,17 +405,20 @@ __global__ void __launch_bounds__(kThreads) norm_dx_kernel(const __grid_constant
   }
   __syncthreads();
   if (!k.here) return;
-  float mean[V], rstd[V], w[V], o[V], m0[V], m1[V];
+  float mean[K], rstd[K], m0[K], m1[K], w[V], o[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int g = (k.c + i) / p.n;
+  for (int i = 0; i < K; ++i) {
+    const int g = (k.c + i * Q) / p.n;
     const float2 m = reinterpret_cast<const float2*>(p.stats)[int64_t(b) * p.G + g];
     mean[i] = m.x;
     rstd[i] = m.y;
-    w[i] = p.weight ? p.weight[k.c + i] : 1.f;
-    o[i] = p.bias ? p.bias[k.c + i] : 0.f;
     m0[i] = known[g - g0].x;
     m1[i] = known[g - g0].y;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    w[i] = p.weight ? p.weight[k.c + i] : 1.f;
+    o[i] = p.bias ? p.bias[k.c + i] : 0.f;
   }
   const int64_t t0 = rb * p.range, tokens = min(p.range, p.N - t0);
   const T* x = static_cast<const T*>(p.x) + k.at(p.xs, b) + (t0 + row) * p.xs[2];
@@ -420,9 +441,9 @@ __global__ void __launch_bounds__(kThreads) norm_dx_kernel(const __grid_constant
         d[e].open(g);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const float xhat = (f[i] - mean[i]) * rstd[i];
+          const float xhat = (f[i] - mean[i / Q]) * rstd[i / Q];
           const float q = g[i] * act_grad<T, ACT>(fmaf(xhat, w[i], o[i])) * w[i];
-          f[i] = rstd[i] * (q - m0[i] - xhat * m1[i]);
+          f[i] = rstd[i / Q] * (q - m0[i / Q] - xhat * m1[i / Q]);
         }
         v[e].close(f);
         v[e].store(dx + (j + e) * p.rows * p.dxs[2]);
@@ -589,29 +610,32 @@ struct Cut {
 };
 constexpr int kSmallBytes = 96 * 1024;        // of a group in shared memory, as fp32
 constexpr int64_t kSmallTotal = 1 << 21;      // values in all, above which SMs are full either way
-Cut cut_of(int32_t B, int64_t N, int C, int G, int V, bool backward) {
+// of 256 threads over a row's vectors
+void share(Cut& k, int vectors) {
+  k.lanes = std::min(vectors, kThreads);
+  k.rows = std::max(1, kThreads / k.lanes);
+}
+// one block a group; V divides the group's channels
+Cut cut_small(int64_t N, int n, int V, bool backward) {
   Cut k{};
-  const int n = C / G;
-  const int64_t values = N * n;
-  const auto share = [&](int vectors) {  // of 256 threads over a row's vectors
-    k.lanes = std::min(vectors, kThreads);
-    k.rows = std::max(1, kThreads / k.lanes);
-  };
-  if (n % V == 0 && B * N * C <= kSmallTotal) {
-    share(n / V);
-    k.rows = int(std::min<int64_t>(k.rows, N));
-    const int64_t bytes = backward ? values * 8 + int64_t(k.rows) * n * 8 : values * 4;
-    if (bytes <= kSmallBytes) {
-      k.small = true;
-      k.smem = int(bytes);
-      k.row_blocks = k.col_blocks = 1;
-      return k;
-    }
-  }
+  share(k, n / V);
+  k.rows = int(std::min<int64_t>(k.rows, N));
+  k.small = true;
+  k.smem = int(N * n * (backward ? 8 : 4) + (backward ? int64_t(k.rows) * n * 8 : 0));
+  k.row_blocks = k.col_blocks = 1;
+  return k;
+}
+bool fits_small(int32_t B, int64_t N, int C, int n, bool backward) {
+  // with a row of sums a thread at most, 2 kThreads floats a channel vector of one
+  const int64_t bytes = N * n * (backward ? 8 : 4) + (backward ? int64_t(std::max(n, kThreads)) * 8 * 8 : 0);
+  return B * N * C <= kSmallTotal && bytes <= kSmallBytes;
+}
+Cut cut_blocks(int32_t B, int64_t N, int C, int G, int V) {
+  Cut k{};
   const int vectors = C / V;
   k.col_blocks = (vectors + kThreads - 1) / kThreads;
-  share((vectors + k.col_blocks - 1) / k.col_blocks);
-  k.slots = std::min(G, k.lanes * V / n + 2);
+  share(k, (vectors + k.col_blocks - 1) / k.col_blocks);
+  k.slots = std::min(G, k.lanes * V / (C / G) + 2);
   // four blocks an SM in all, of at least 32 tokens a thread
   const int64_t most = std::max<int64_t>(1, 4 * 148 / (int64_t(B) * k.col_blocks));
   const int64_t blocks = std::min<int64_t>(most, (N + k.rows * kRun - 1) / (k.rows * kRun));
@@ -638,59 +662,60 @@ bool allow_smem(F* kernel, OncePerDevice& once) {
 }
 
 template <class T, int BYTES, int ACT>
-int launch_forward(NormArgs& a, const Cut& k, cudaStream_t st) {
-  if (k.small) {
-    static OncePerDevice once;
-    const auto f = norm_small_kernel<T, BYTES, ACT>;
-    if (!allow_smem(f, once)) return TTT_ERR_CUDA;
-    f<<<dim3(a.G, a.B), kThreads, k.smem, st>>>(a);
-  } else {
-    const dim3 grid(k.col_blocks, k.row_blocks, a.B);
-    norm_parts_kernel<T, BYTES><<<grid, kThreads, k.smem, st>>>(a);
-    norm_apply_kernel<T, BYTES, ACT><<<grid, kThreads, k.slots * 8, st>>>(a);
-  }
+int launch_small(bool backward, NormArgs& a, const Cut& k, cudaStream_t st) {
+  static OncePerDevice once[2];
+  const auto f = backward ? norm_small_grad_kernel<T, BYTES, ACT> : norm_small_kernel<T, BYTES, ACT>;
+  if (!allow_smem(f, once[backward])) return TTT_ERR_CUDA;
+  f<<<dim3(a.G, a.B), kThreads, k.smem, st>>>(a);
+  if (backward && (a.dweight || a.dbias)) norm_join_sums_kernel<<<(a.C + 31) / 32, 1024, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
 }
-template <class T, int BYTES, int ACT>
-int launch_backward(NormArgs& a, const Cut& k, cudaStream_t st) {
-  if (k.small) {
-    static OncePerDevice once;
-    const auto f = norm_small_grad_kernel<T, BYTES, ACT>;
-    if (!allow_smem(f, once)) return TTT_ERR_CUDA;
-    f<<<dim3(a.G, a.B), kThreads, k.smem, st>>>(a);
-    if (a.dweight || a.dbias) norm_join_sums_kernel<<<(a.C + 31) / 32, 1024, 0, st>>>(a);
-  } else {
-    const dim3 grid(k.col_blocks, k.row_blocks, a.B);
-    norm_sums_kernel<T, BYTES, ACT><<<grid, kThreads, k.smem, st>>>(a);
+template <class T, int BYTES, int Q, int ACT>
+int launch_blocks(bool backward, NormArgs& a, const Cut& k, cudaStream_t st) {
+  const dim3 grid(k.col_blocks, k.row_blocks, a.B);
+  if (backward) {
+    norm_sums_kernel<T, BYTES, Q, ACT><<<grid, kThreads, k.smem, st>>>(a);
     norm_join_sums_kernel<<<(a.C + 31) / 32, 1024, 0, st>>>(a);
-    norm_dx_kernel<T, BYTES, ACT><<<grid, kThreads, k.slots * 8, st>>>(a);
+    norm_dx_kernel<T, BYTES, Q, ACT><<<grid, kThreads, k.slots * 8, st>>>(a);
+  } else {
+    norm_parts_kernel<T, BYTES, Q><<<grid, kThreads, k.smem, st>>>(a);
+    norm_apply_kernel<T, BYTES, Q, ACT><<<grid, kThreads, k.slots * 8, st>>>(a);
   }
   return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
 }
-
+// Q: channels of a vector that are of one group for certain
+template <class T, int BYTES, int ACT>
+int launch_act(bool backward, NormArgs& a, const Cut& k, cudaStream_t st) {
+  constexpr int V = BYTES / int(sizeof(T));
+  if (k.small) return launch_small<T, BYTES, ACT>(backward, a, k, st);
+  if constexpr (BYTES == 16) {
+    if (a.n % V == 0) return launch_blocks<T, BYTES, V, ACT>(backward, a, k, st);
+    if constexpr (V == 8)
+      if (a.n % 4 == 0) return launch_blocks<T, BYTES, 4, ACT>(backward, a, k, st);
+  }
+  return launch_blocks<T, BYTES, 1, ACT>(backward, a, k, st);
+}
 template <class T, int BYTES>
-int launch_act(bool backward, int act, NormArgs& a, const Cut& k, cudaStream_t st) {
+int launch(bool backward, int act, NormArgs& a, const Cut& k, cudaStream_t st) {
   switch (act) {
-    case TTT_ACT_SILU:
-      return backward ? launch_backward<T, BYTES, TTT_ACT_SILU>(a, k, st) : launch_forward<T, BYTES, TTT_ACT_SILU>(a, k, st);
-    case TTT_ACT_GELU:
-      return backward ? launch_backward<T, BYTES, TTT_ACT_GELU>(a, k, st) : launch_forward<T, BYTES, TTT_ACT_GELU>(a, k, st);
-    default:
-      return backward ? launch_backward<T, BYTES, TTT_ACT_NONE>(a, k, st) : launch_forward<T, BYTES, TTT_ACT_NONE>(a, k, st);
+    case TTT_ACT_SILU: return launch_act<T, BYTES, TTT_ACT_SILU>(backward, a, k, st);
+    case TTT_ACT_GELU: return launch_act<T, BYTES, TTT_ACT_GELU>(backward, a, k, st);
+    default: return launch_act<T, BYTES, TTT_ACT_NONE>(backward, a, k, st);
   }
 }
 
-// The widest vectors that all rows start on and that groups (where they lie apart) or rows
-// are whole numbers of.
-int vector_bytes(const RowTensor* t, int nt, const ttt_strides* const* s, int C, int n, int elem) {
+// Vectors of 16 or 4 bytes or of one channel: the widest that all rows start on and that
+// groups (where they lie apart, or each has a block of its own) or rows are whole numbers of.
+int vector_bytes(const RowTensor* t, int nt, const ttt_strides* const* s, int C, int n, int elem, bool each) {
   int wide = 16;
+  const auto narrower = [&] { wide = wide == 16 ? 4 : elem; };
   for (int i = 0; i < nt; ++i) {
     const bool together = s[i]->head == n || n == C;  // a row's groups follow one another
-    while (wide > elem && (C * elem % wide || (!together && n * elem % wide))) wide /= 2;
+    while (wide > elem && (C * elem % wide || ((!together || each) && n * elem % wide))) narrower();
     // channels last: rows are aligned by their first group
     RowTensor rows = t[i];
     if (together) rows.n[1] = 1;
-    while (wide > elem && !rows_aligned(rows, wide)) wide /= 2;
+    while (wide > elem && !rows_aligned(rows, wide)) narrower();
   }
   return wide;
 }
@@ -737,10 +762,11 @@ void put_strides(int64_t (&to)[3], const ttt_strides* s) { to[0] = s->batch, to[
 size_t space_needed(const ttt_norm* h, int32_t B, int64_t N, bool backward) {
   const ttt_norm_config& c = h->cfg;
   const int elem = c.dtype == TTT_BF16 ? 2 : 4;
+  if (fits_small(B, N, c.C, c.C / c.groups, backward)) return workspace_of(cut_small(N, 1, 1, backward), B, c.C, backward);
   size_t most = 0;
-  for (int wide = 16; wide >= elem; wide /= 2)
+  for (int wide : {16, 4, elem})
     if (c.C * elem % wide == 0)
-      most = std::max(most, workspace_of(cut_of(B, N, c.C, c.groups, wide / elem, backward), B, c.C, backward));
+      most = std::max(most, workspace_of(cut_blocks(B, N, c.C, c.groups, wide / elem), B, c.C, backward));
   return most;
 }
 
@@ -750,8 +776,9 @@ int run(const ttt_norm* h, bool backward, NormArgs& a, const RowTensor* t, const
   const ttt_norm_config& c = h->cfg;
   a.C = c.C, a.G = c.groups, a.n = c.C / c.groups, a.eps = c.eps;
   const int elem = c.dtype == TTT_BF16 ? 2 : 4;
-  const int wide = vector_bytes(t, nt, s, c.C, a.n, elem);
-  const Cut k = cut_of(a.B, a.N, c.C, c.groups, wide / elem, backward);
+  const bool small = fits_small(a.B, a.N, c.C, a.n, backward);
+  const int wide = vector_bytes(t, nt, s, c.C, a.n, elem, small);
+  const Cut k = small ? cut_small(a.N, a.n, wide / elem, backward) : cut_blocks(a.B, a.N, c.C, c.groups, wide / elem);
   put_cut(a, k);
   if (backward) {
     a.part_sums = static_cast<float*>(workspace);
@@ -760,13 +787,10 @@ int run(const ttt_norm* h, bool backward, NormArgs& a, const RowTensor* t, const
     a.parts = static_cast<float2*>(workspace);
   }
   if (elem == 2)
-    return wide == 16  ? launch_act<__nv_bfloat16, 16>(backward, c.act, a, k, st)
-           : wide == 8 ? launch_act<__nv_bfloat16, 8>(backward, c.act, a, k, st)
-           : wide == 4 ? launch_act<__nv_bfloat16, 4>(backward, c.act, a, k, st)
-                       : launch_act<__nv_bfloat16, 2>(backward, c.act, a, k, st);
-  return wide == 16  ? launch_act<float, 16>(backward, c.act, a, k, st)
-         : wide == 8 ? launch_act<float, 8>(backward, c.act, a, k, st)
-                     : launch_act<float, 4>(backward, c.act, a, k, st);
+    return wide == 16  ? launch<__nv_bfloat16, 16>(backward, c.act, a, k, st)
+           : wide == 4 ? launch<__nv_bfloat16, 4>(backward, c.act, a, k, st)
+                       : launch<__nv_bfloat16, 2>(backward, c.act, a, k, st);
+  return wide == 16 ? launch<float, 16>(backward, c.act, a, k, st) : launch<float, 4>(backward, c.act, a, k, st);
 }
 
 }  // namespace
