@@ -374,6 +374,19 @@ NORM = [
     (1, 40, 2048, 16, "silu", "f32", "tokens"),
     (9, 33, 24, 3, "gelu", "bf16", "heads"),
     (1, 5, 1032, 8, "none", "bf16", "tokens"),
+    # groups too large for one block: vectors of one group, of two, of several, groups over two blocks of
+    # channels, more channels than a block has, rows of a block that stay empty, narrow vectors
+    (2, 4100, 96, 6, "silu", "bf16", "tokens"),
+    (1, 8200, 128, 32, "silu", "bf16", "tokens"),
+    (1, 9001, 96, 32, "gelu", "f32", "tokens"),
+    (1, 7000, 96, 32, "none", "bf16", "tokens"),
+    (1, 400, 4128, 3, "silu", "bf16", "tokens"),
+    (1, 300, 4100, 2, "gelu", "f32", "tokens"),
+    (2, 1100, 384, 3, "silu", "bf16", "heads"),
+    (3, 2050, 90, 5, "silu", "bf16", "tokens"),
+    (2, 3333, 35, 1, "none", "bf16", "heads"),
+    (1, 2500, 132, 2, "silu", "f32", "slice"),
+    (2, 3000, 40, 2, "gelu", "bf16", "odd"),
 ]
 
 

@@ -33,15 +33,15 @@ struct NormArgs {
   void *y, *dx;
   const float *weight, *bias;
   float *stats, *dweight, *dbias;        // stats [B][G][2]
-  float2* parts;                         // forward: (mean, S) of each block's part of a group
-  float *part_sums, *sums;               // backward: [B][blocks][C][2]; [B][C][2]
+  float2* parts;         // of each block and group: forward (mean, S), backward (sum q, sum q xhat)
+  float2* channel_sums;  // backward: [B][ranges][C] (sum dz, sum dz xhat)
   int64_t xs[3], ys[3], dys[3], dxs[3];  // batch, group, token
   int64_t N;
   int32_t B, C, G, n;                    // n channels a group
   float eps;
   int32_t lanes, rows;                   // a block's vectors of channels, and tokens at a time
   int32_t col_blocks, row_blocks;        // blocks of channels; ranges of tokens
-  int64_t range;                         // tokens of a range
+  int32_t range;                         // tokens of a range
   int32_t slots;                         // groups of a block of channels at most
 };
 
@@ -70,33 +70,38 @@ __device__ __forceinline__ float2 finish(const Part& v, float eps) {  // mean, 1
 
 // sigma(z).  bf16 outputs take the hardware's exponential (2^-22 off, and 2^-24 of the
 // exponent's size), fp32 ones the library's; the reciprocal is the hardware's, 2^-23 off.
-__device__ __forceinline__ float rcp_fast(float v) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-template <class T>
-__device__ __forceinline__ float sigmoid(float z) {
-  if (sizeof(T) == 4) return rcp_fast(1.f + expf(-z));
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
-  return rcp_fast(1.f + e);
+template <class T, class P>
+__device__ __forceinline__ P sigmoid(P z) {
+  P e;
+  if constexpr (sizeof(T) == 4)
+    e = each(z, [](float v) { return expf(-v); });
+  else
+    e = each(mul_(z, P::all(-1.4426950408889634f)), [](float v) { return exp2_fast(v); });
+  return each(add_(e, P::all(1.f)), [](float v) { return rcp_fast(v); });
 }
 constexpr float kInvSqrt2 = 0.70710678118654752f, kInvSqrt2Pi = 0.39894228040143268f;
-template <class T, int ACT>
-__device__ __forceinline__ float act(float z) {
-  if (ACT == TTT_ACT_SILU) return z * sigmoid<T>(z);
-  if (ACT == TTT_ACT_GELU) return 0.5f * z * erfcf(-z * kInvSqrt2);
+template <class P>
+__device__ __forceinline__ P normal_cdf(P z) {
+  return each(z, [](float v) { return 0.5f * erfcf(v * -kInvSqrt2); });
+}
+template <class T, int ACT, class P>
+__device__ __forceinline__ P act(P z) {
+  if constexpr (ACT == TTT_ACT_SILU) return mul_(z, sigmoid<T>(z));
+  if constexpr (ACT == TTT_ACT_GELU) return mul_(z, normal_cdf(z));
   return z;
 }
-template <class T, int ACT>
-__device__ __forceinline__ float act_grad(float z) {
-  if (ACT == TTT_ACT_SILU) {
-    const float s = sigmoid<T>(z);
-    return fmaf(z * s, 1.f - s, s);
+// the activation's slope at z, times dy
+template <class T, int ACT, class P>
+__device__ __forceinline__ P act_grad(P z, P dy) {
+  if constexpr (ACT == TTT_ACT_SILU) {
+    const P s = sigmoid<T>(z);
+    return mul_(dy, fma_(mul_(z, s), sub_(P::all(1.f), s), s));
   }
-  if (ACT == TTT_ACT_GELU) return fmaf(z * kInvSqrt2Pi, expf(-0.5f * z * z), 0.5f * erfcf(-z * kInvSqrt2));
-  return 1.f;
+  if constexpr (ACT == TTT_ACT_GELU) {
+    const P d = each(z, [](float v) { return kInvSqrt2Pi * expf(-0.5f * v * v); });
+    return mul_(dy, fma_(z, d, normal_cdf(z)));
+  }
+  return dy;
 }
 
 // Where a thread's vector of channels lies
@@ -124,20 +129,22 @@ __device__ __forceinline__ int block_end(const NormArgs& p, int col_block, int V
 template <class T, int BYTES, int Q>
 __global__ void __launch_bounds__(kThreads, 3) norm_parts_kernel(const __grid_constant__ NormArgs p) {
   using X = Vec<T, BYTES>;
-  constexpr int V = X::N, K = V / Q, kAtOnce = 8;
+  using P = typename X::P;
+  constexpr int V = X::N, K = V / Q, kPacks = X::kPacks, kSums = Q > 1 ? K : kPacks, kAtOnce = 8;
   extern __shared__ float2 threads[];  // [row][sum of the block]
   const int cb = blockIdx.x, rb = blockIdx.y, b = blockIdx.z;
   const Column k = column(p, cb, V);
   const int row = threadIdx.x / p.lanes;
-  const int64_t t0 = rb * p.range, tokens = min(p.range, p.N - t0);
+  const int64_t t0 = int64_t(rb) * p.range;
+  const int tokens = int(min(int64_t(p.range), p.N - t0));
   const int width = p.lanes * V;
   if (k.here) {
     const T* x = static_cast<const T*>(p.x) + k.at(p.xs, b) + (t0 + row) * p.xs[2];
     const int64_t hop = p.rows * p.xs[2];
     float count = 0.f, mean[K] = {}, S[K] = {};
-    for (int64_t left = tokens > row ? (tokens - row + p.rows - 1) / p.rows : 0; left > 0;) {
-      const int run = left < kRun ? int(left) : kRun;
-      float first[K], s[K], q[K];
+    for (int left = tokens > row ? (tokens - row + p.rows - 1) / p.rows : 0; left > 0;) {
+      const int run = min(left, kRun);
+      P off[kPacks], s[kSums], q[kSums];  // off: less the run's first value; a pack's sums side by side
       for (int j = 0; j < run; j += kAtOnce) {
         X v[kAtOnce];
 #pragma unroll
@@ -149,28 +156,38 @@ __global__ void __launch_bounds__(kThreads, 3) norm_parts_kernel(const __grid_co
           float f[V];
           v[0].open(f);
 #pragma unroll
-          for (int i = 0; i < K; ++i) first[i] = f[i * Q], s[i] = 0.f, q[i] = 0.f;
+          for (int i = V - 1; i >= 0; --i) f[i] = -f[Q > 1 ? i / Q * Q : i];  // a sum's first is the last to change
+#pragma unroll
+          for (int i = 0; i < kPacks; ++i) off[i] = P::of(f + i * P::N);
+#pragma unroll
+          for (int i = 0; i < kSums; ++i) s[i] = P::all(0.f), q[i] = P::all(0.f);
         }
 #pragma unroll
         for (int e = 0; e < kAtOnce; ++e)
           if (j + e < run) {
-            float f[V];
+            P f[kPacks];
             v[e].open(f);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-              const float d = f[i] - first[i / Q];
-              s[i / Q] += d;
-              q[i / Q] = fmaf(d, d, q[i / Q]);
+            for (int i = 0; i < kPacks; ++i) {
+              const P d = add_(f[i], off[i]);
+              constexpr int kEach = kPacks / kSums;  // packs to a sum
+              s[i / kEach] = add_(s[i / kEach], d);
+              q[i / kEach] = fma_(d, d, q[i / kEach]);
             }
           }
       }
       const float n = float(run * Q), inv = 1.f / n, all = count + n, f = n / all;
 #pragma unroll
       for (int i = 0; i < K; ++i) {
-        const float m = s[i] * inv, Si = fmaxf(fmaf(-s[i], m, q[i]), 0.f);
-        const float d = first[i] + m - mean[i];
+        // Q > 1: both halves of a pack are of one sum
+        const int w = Q > 1 ? i : i / P::N;
+        const float sum = Q > 1 && P::N == 2 ? s[w][0] + s[w][P::N - 1] : s[w][i % P::N];
+        const float squares = Q > 1 && P::N == 2 ? q[w][0] + q[w][P::N - 1] : q[w][i % P::N];
+        const float first = -off[i * Q / P::N][i * Q % P::N];
+        const float m = sum * inv, Si = fmaxf(fmaf(-sum, m, squares), 0.f);
+        const float d = first + m - mean[i];
         if (count == 0.f) {
-          mean[i] = first[i] + m;
+          mean[i] = first + m;
           S[i] = Si;
         } else {
           mean[i] = fmaf(d, f, mean[i]);
@@ -210,8 +227,7 @@ __device__ __forceinline__ float2 join_parts(const NormArgs& p, int b, int g, in
   for (int e = lane; e < p.row_blocks * blocks; e += 32) {
     const int rb = e / blocks, cb = first + e % blocks;
     const int c0 = cb * width, c1 = min(p.C, c0 + width);
-    const int64_t tokens = min(p.range, p.N - rb * p.range);
-    const float n = float(tokens) * float(min((g + 1) * p.n, c1) - max(g * p.n, c0));
+    const float n = float(min(int64_t(p.range), p.N - int64_t(rb) * p.range)) * float(min((g + 1) * p.n, c1) - max(g * p.n, c0));
     const float2 m = p.parts[((int64_t(b) * p.row_blocks + rb) * p.col_blocks + cb) * p.slots + g - c0 / p.n];
     v = join(v, {n, m.x, m.y});
   }
@@ -222,7 +238,9 @@ __device__ __forceinline__ float2 join_parts(const NormArgs& p, int b, int g, in
 template <class T, int BYTES, int Q, int ACT>
 __global__ void __launch_bounds__(kThreads, 3) norm_apply_kernel(const __grid_constant__ NormArgs p) {
   using X = Vec<T, BYTES>;
-  constexpr int V = X::N, K = V / Q, kAtOnce = 8;
+  using P = typename X::P;
+  // a pack's mean is shared by the packs of kStep channels
+  constexpr int V = X::N, K = V / Q, kPacks = X::kPacks, kStep = Q > P::N ? Q : P::N, kMeans = V / kStep, kAtOnce = 8;
   extern __shared__ float2 known[];  // (mean, 1 / std) of the block's groups
   const int cb = gridDim.x - 1 - blockIdx.x, rb = gridDim.y - 1 - blockIdx.y, b = gridDim.z - 1 - blockIdx.z;
   const Column k = column(p, cb, V);
@@ -238,69 +256,108 @@ __global__ void __launch_bounds__(kThreads, 3) norm_apply_kernel(const __grid_co
   }
   __syncthreads();
   if (!k.here) return;
-  float mean[K], scale[V], shift[V];
+  float2 m[K];
 #pragma unroll
-  for (int j = 0; j < K; ++j) {
-    const float2 m = known[(k.c + j * Q) / p.n - g0];
-    mean[j] = m.x;
+  for (int j = 0; j < K; ++j) m[j] = known[(k.c + j * Q) / p.n - g0];
+  P mean[kMeans], scale[kPacks], shift[kPacks];  // mean: negative
 #pragma unroll
-    for (int i = j * Q; i < (j + 1) * Q; ++i) {
-      scale[i] = m.y * (p.weight ? p.weight[k.c + i] : 1.f);
-      shift[i] = p.bias ? p.bias[k.c + i] : 0.f;
+  for (int i = 0; i < V; i += P::N) {
+    float a[P::N], s[P::N], o[P::N];
+#pragma unroll
+    for (int e = 0; e < P::N; ++e) {
+      a[e] = -m[(i + e) / Q].x;
+      s[e] = m[(i + e) / Q].y * (p.weight ? p.weight[k.c + i + e] : 1.f);
+      o[e] = p.bias ? p.bias[k.c + i + e] : 0.f;
     }
+    mean[i / kStep] = P::of(a);
+    scale[i / P::N] = P::of(s);
+    shift[i / P::N] = P::of(o);
   }
-  const int64_t t0 = rb * p.range, tokens = min(p.range, p.N - t0);
+  const int64_t t0 = int64_t(rb) * p.range;
+  const int tokens = int(min(int64_t(p.range), p.N - t0));
   const T* x = static_cast<const T*>(p.x) + k.at(p.xs, b) + (t0 + row) * p.xs[2];
   T* y = static_cast<T*>(p.y) + k.at(p.ys, b) + (t0 + row) * p.ys[2];
-  const int64_t mine = tokens > row ? (tokens - row + p.rows - 1) / p.rows : 0;
-  for (int64_t j = (mine + kAtOnce - 1) / kAtOnce * kAtOnce - kAtOnce; j >= 0; j -= kAtOnce) {
+  const int mine = tokens > row ? (tokens - row + p.rows - 1) / p.rows : 0;
+  const int64_t hop = p.rows * p.xs[2], yhop = p.rows * p.ys[2];
+  x += (mine - 1) * hop;
+  y += (mine - 1) * yhop;
+  for (int left = mine; left > 0; left -= kAtOnce) {  // last to first
     X v[kAtOnce];
 #pragma unroll
-    for (int e = 0; e < kAtOnce; ++e)
-      if (j + e < mine) v[e].load(x + (j + e) * p.rows * p.xs[2]);
+    for (int e = 0; e < kAtOnce; ++e) {
+      if (e < left) v[e].load(x);
+      x -= e < left ? hop : 0;
+    }
 #pragma unroll
-    for (int e = 0; e < kAtOnce; ++e)
-      if (j + e < mine) {
-        float f[V];
+    for (int e = 0; e < kAtOnce; ++e) {
+      if (e < left) {
+        P f[kPacks];
         v[e].open(f);
 #pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = act<T, ACT>(fmaf(f[i] - mean[i / Q], scale[i], shift[i]));
+        for (int i = 0; i < kPacks; ++i)
+          f[i] = act<T, ACT>(fma_(add_(f[i], mean[i * P::N / kStep]), scale[i], shift[i]));
         v[e].close(f);
-        v[e].store(y + (j + e) * p.rows * p.ys[2]);
+        v[e].store(y);
       }
+      y -= yhop;
+    }
   }
 }
+
+// What the backward kernels know of a thread's channels: mean (negative) and 1 / std, one of
+// each for the packs of kStep channels, weight and bias
+template <class P, int PACKS, int MEANS>
+struct Known {
+  P mean[MEANS], rstd[MEANS], weight[PACKS], bias[PACKS];
+  template <int STEP>
+  __device__ __forceinline__ void load(const NormArgs& p, int b, int c) {
+#pragma unroll
+    for (int i = 0; i < PACKS; ++i) {
+      float m[P::N], r[P::N], w[P::N], o[P::N];
+#pragma unroll
+      for (int e = 0; e < P::N; ++e) {
+        const int k = c + i * P::N + e;
+        const float2 s = reinterpret_cast<const float2*>(p.stats)[int64_t(b) * p.G + k / p.n];
+        m[e] = -s.x;
+        r[e] = s.y;
+        w[e] = p.weight ? p.weight[k] : 1.f;
+        o[e] = p.bias ? p.bias[k] : 0.f;
+      }
+      mean[i * P::N / STEP] = P::of(m);
+      rstd[i * P::N / STEP] = P::of(r);
+      weight[i] = P::of(w);
+      bias[i] = P::of(o);
+    }
+  }
+};
 
 // Backward, of one range of tokens and block of channels: each channel's sums of dz and dz xhat
 template <class T, int BYTES, int Q, int ACT>
 __global__ void __launch_bounds__(kThreads, 2) norm_sums_kernel(const __grid_constant__ NormArgs p) {
   using X = Vec<T, BYTES>;
-  constexpr int V = X::N, K = V / Q, kAtOnce = 4;
+  using P = typename X::P;
+  constexpr int V = X::N, kPacks = X::kPacks, kStep = Q > P::N ? Q : P::N, kMeans = V / kStep, kAtOnce = 4;
   extern __shared__ float2 threads[];
   const int cb = blockIdx.x, rb = blockIdx.y, b = blockIdx.z;
   const Column k = column(p, cb, V);
   const int row = threadIdx.x / p.lanes;
-  const int64_t t0 = rb * p.range, tokens = min(p.range, p.N - t0);
+  const int64_t t0 = int64_t(rb) * p.range;
+  const int tokens = int(min(int64_t(p.range), p.N - t0));
   const int width = p.lanes * V;
   if (k.here) {
-    float mean[K], rstd[K], w[V], o[V], total0[V] = {}, total1[V] = {};
+    Known<P, kPacks, kMeans> q;
+    q.template load<kStep>(p, b, k.c);
+    P total0[kPacks], total1[kPacks];
 #pragma unroll
-    for (int i = 0; i < K; ++i) {
-      const float2 m = reinterpret_cast<const float2*>(p.stats)[int64_t(b) * p.G + (k.c + i * Q) / p.n];
-      mean[i] = m.x;
-      rstd[i] = m.y;
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      w[i] = p.weight ? p.weight[k.c + i] : 1.f;
-      o[i] = p.bias ? p.bias[k.c + i] : 0.f;
-    }
+    for (int i = 0; i < kPacks; ++i) total0[i] = total1[i] = P::all(0.f);
     const T* x = static_cast<const T*>(p.x) + k.at(p.xs, b) + (t0 + row) * p.xs[2];
     const T* dy = static_cast<const T*>(p.dy) + k.at(p.dys, b) + (t0 + row) * p.dys[2];
     const int64_t hop = p.rows * p.xs[2], dhop = p.rows * p.dys[2];
-    for (int64_t left = tokens > row ? (tokens - row + p.rows - 1) / p.rows : 0; left > 0;) {
-      const int run = left < kRun ? int(left) : kRun;  // sums of runs, so that no long sum swallows its terms
-      float s0[V] = {}, s1[V] = {};
+    for (int left = tokens > row ? (tokens - row + p.rows - 1) / p.rows : 0; left > 0;) {
+      const int run = min(left, kRun);  // sums of runs, so that no long sum swallows its terms
+      P s0[kPacks], s1[kPacks];
+#pragma unroll
+      for (int i = 0; i < kPacks; ++i) s0[i] = s1[i] = P::all(0.f);
       for (int j = 0; j < run; j += kAtOnce) {
         X v[kAtOnce], d[kAtOnce];
 #pragma unroll
@@ -315,68 +372,73 @@ __global__ void __launch_bounds__(kThreads, 2) norm_sums_kernel(const __grid_con
 #pragma unroll
         for (int e = 0; e < kAtOnce; ++e)
           if (j + e < run) {
-            float f[V], g[V];
+            P f[kPacks], g[kPacks];
             v[e].open(f);
             d[e].open(g);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-              const float xhat = (f[i] - mean[i / Q]) * rstd[i / Q];
-              const float dz = g[i] * act_grad<T, ACT>(fmaf(xhat, w[i], o[i]));
-              s0[i] += dz;
-              s1[i] = fmaf(dz, xhat, s1[i]);
+            for (int i = 0; i < kPacks; ++i) {
+              const P xhat = mul_(add_(f[i], q.mean[i * P::N / kStep]), q.rstd[i * P::N / kStep]);
+              const P dz = act_grad<T, ACT>(fma_(xhat, q.weight[i], q.bias[i]), g[i]);
+              s0[i] = add_(s0[i], dz);
+              s1[i] = fma_(dz, xhat, s1[i]);
             }
           }
       }
 #pragma unroll
-      for (int i = 0; i < V; ++i) total0[i] += s0[i], total1[i] += s1[i];
+      for (int i = 0; i < kPacks; ++i) total0[i] = add_(total0[i], s0[i]), total1[i] = add_(total1[i], s1[i]);
       left -= run;
     }
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      threads[row * width + (threadIdx.x % p.lanes) * V + i] = make_float2(total0[i], total1[i]);
+      threads[row * width + (threadIdx.x % p.lanes) * V + i] =
+          make_float2(total0[i / P::N][i % P::N], total1[i / P::N][i % P::N]);
   }
   __syncthreads();
-  const int c0 = cb * width, c1 = block_end(p, cb, V);
+  const int c0 = cb * width, c1 = block_end(p, cb, V), g0 = c0 / p.n;
   for (int c = threadIdx.x; c < c1 - c0; c += kThreads) {
     float2 s = threads[c];
     for (int r = 1; r < p.rows; ++r) {
       s.x += threads[r * width + c].x;
       s.y += threads[r * width + c].y;
     }
-    reinterpret_cast<float2*>(p.part_sums)[(int64_t(b) * p.row_blocks + rb) * p.C + c0 + c] = s;
+    p.channel_sums[(int64_t(b) * p.row_blocks + rb) * p.C + c0 + c] = s;
+    threads[c] = s;
+  }
+  __syncthreads();
+  // of each group the sums of q = dz weight and q xhat over this block
+  for (int g = g0 + threadIdx.x / 32; g <= (c1 - 1) / p.n; g += kThreads / 32) {
+    float q0 = 0.f, q1 = 0.f;
+    for (int c = max(g * p.n, c0) + threadIdx.x % 32; c < min((g + 1) * p.n, c1); c += 32) {
+      const float w = p.weight ? p.weight[c] : 1.f;
+      q0 = fmaf(threads[c - c0].x, w, q0);
+      q1 = fmaf(threads[c - c0].y, w, q1);
+    }
+#pragma unroll
+    for (int m = 16; m; m /= 2) q0 += __shfl_xor_sync(~0u, q0, m), q1 += __shfl_xor_sync(~0u, q1, m);
+    if (threadIdx.x % 32 == 0)
+      p.parts[((int64_t(b) * p.row_blocks + rb) * p.col_blocks + cb) * p.slots + g - g0] = make_float2(q0, q1);
   }
 }
 
-// Joins the ranges' sums, 32 channels a block: sums [B][C], and over the batch dweight and dbias
-__global__ void __launch_bounds__(1024) norm_join_sums_kernel(const __grid_constant__ NormArgs p) {
+// dweight and dbias: the channel sums of all ranges and batch entries, 32 channels a block
+__global__ void __launch_bounds__(1024) norm_dweight_kernel(const __grid_constant__ NormArgs p) {
   __shared__ float2 rows[32][32];
   const int c = blockIdx.x * 32 + threadIdx.x % 32, r = threadIdx.x / 32;
-  const float2* from = reinterpret_cast<const float2*>(p.part_sums);
-  float2 all = make_float2(0.f, 0.f);
-  for (int b = 0; b < p.B; ++b) {
-    float2 s = make_float2(0.f, 0.f);
-    if (c < p.C)
-      for (int rb = r; rb < p.row_blocks; rb += 32) {
-        const float2 v = from[(int64_t(b) * p.row_blocks + rb) * p.C + c];
-        s.x += v.x;
-        s.y += v.y;
-      }
-    rows[r][threadIdx.x % 32] = s;
-    __syncthreads();
-    if (r == 0 && c < p.C) {
-      for (int q = 1; q < min(32, p.row_blocks); ++q) {
-        s.x += rows[q][threadIdx.x].x;
-        s.y += rows[q][threadIdx.x].y;
-      }
-      reinterpret_cast<float2*>(p.sums)[int64_t(b) * p.C + c] = s;
-      all.x += s.x;
-      all.y += s.y;
+  const int64_t all = int64_t(p.B) * p.row_blocks;
+  float2 s = make_float2(0.f, 0.f);
+  if (c < p.C)
+    for (int64_t q = r; q < all; q += 32) {
+      const float2 v = p.channel_sums[q * p.C + c];
+      s.x += v.x;
+      s.y += v.y;
     }
-    __syncthreads();
-  }
+  rows[r][threadIdx.x % 32] = s;
+  __syncthreads();
   if (r == 0 && c < p.C) {
-    if (p.dbias) p.dbias[c] = all.x;
-    if (p.dweight) p.dweight[c] = all.y;
+#pragma unroll
+    for (int q = 1; q < 32; ++q) s.x += rows[q][threadIdx.x].x, s.y += rows[q][threadIdx.x].y;
+    if (p.dbias) p.dbias[c] = s.x;
+    if (p.dweight) p.dweight[c] = s.y;
   }
 }
 
@@ -384,7 +446,8 @@ __global__ void __launch_bounds__(1024) norm_join_sums_kernel(const __grid_const
 template <class T, int BYTES, int Q, int ACT>
 __global__ void __launch_bounds__(kThreads, 2) norm_dx_kernel(const __grid_constant__ NormArgs p) {
   using X = Vec<T, BYTES>;
-  constexpr int V = X::N, K = V / Q, kAtOnce = 4;
+  using P = typename X::P;
+  constexpr int V = X::N, kPacks = X::kPacks, kStep = Q > P::N ? Q : P::N, kMeans = V / kStep, kAtOnce = 4;
   extern __shared__ float2 known[];  // (mean q, mean q xhat) of the block's groups
   const int cb = gridDim.x - 1 - blockIdx.x, rb = gridDim.y - 1 - blockIdx.y, b = gridDim.z - 1 - blockIdx.z;
   const Column k = column(p, cb, V);
@@ -392,12 +455,13 @@ __global__ void __launch_bounds__(kThreads, 2) norm_dx_kernel(const __grid_const
   const int c0 = cb * p.lanes * V, c1 = block_end(p, cb, V), g0 = c0 / p.n;
   const float inv = 1.f / (float(p.N) * float(p.n));
   for (int g = g0 + threadIdx.x / 32; g <= (c1 - 1) / p.n; g += kThreads / 32) {
+    const int width = p.lanes * V, first = g * p.n / width, blocks = ((g + 1) * p.n - 1) / width - first + 1;
     float q0 = 0.f, q1 = 0.f;
-    for (int c = g * p.n + threadIdx.x % 32; c < (g + 1) * p.n; c += 32) {
-      const float w = p.weight ? p.weight[c] : 1.f;
-      const float2 s = reinterpret_cast<const float2*>(p.sums)[int64_t(b) * p.C + c];
-      q0 = fmaf(s.x, w, q0);
-      q1 = fmaf(s.y, w, q1);
+    for (int e = threadIdx.x % 32; e < p.row_blocks * blocks; e += 32) {
+      const int64_t at = (int64_t(b) * p.row_blocks + e / blocks) * p.col_blocks + first + e % blocks;
+      const float2 s = p.parts[at * p.slots + g - (first + e % blocks) * width / p.n];
+      q0 += s.x;
+      q1 += s.y;
     }
 #pragma unroll
     for (int m = 16; m; m /= 2) q0 += __shfl_xor_sync(~0u, q0, m), q1 += __shfl_xor_sync(~0u, q1, m);
@@ -405,49 +469,60 @@ __global__ void __launch_bounds__(kThreads, 2) norm_dx_kernel(const __grid_const
   }
   __syncthreads();
   if (!k.here) return;
-  float mean[K], rstd[K], m0[K], m1[K], w[V], o[V];
+  Known<P, kPacks, kMeans> q;
+  q.template load<kStep>(p, b, k.c);
+  P m0[kMeans], m1[kMeans];  // negative
 #pragma unroll
-  for (int i = 0; i < K; ++i) {
-    const int g = (k.c + i * Q) / p.n;
-    const float2 m = reinterpret_cast<const float2*>(p.stats)[int64_t(b) * p.G + g];
-    mean[i] = m.x;
-    rstd[i] = m.y;
-    m0[i] = known[g - g0].x;
-    m1[i] = known[g - g0].y;
-  }
+  for (int i = 0; i < V; i += P::N) {
+    float a[P::N], d[P::N];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    w[i] = p.weight ? p.weight[k.c + i] : 1.f;
-    o[i] = p.bias ? p.bias[k.c + i] : 0.f;
+    for (int e = 0; e < P::N; ++e) {
+      const float2 m = known[(k.c + i + e) / p.n - g0];
+      a[e] = -m.x;
+      d[e] = -m.y;
+    }
+    m0[i / kStep] = P::of(a);
+    m1[i / kStep] = P::of(d);
   }
-  const int64_t t0 = rb * p.range, tokens = min(p.range, p.N - t0);
+  const int64_t t0 = int64_t(rb) * p.range;
+  const int tokens = int(min(int64_t(p.range), p.N - t0));
   const T* x = static_cast<const T*>(p.x) + k.at(p.xs, b) + (t0 + row) * p.xs[2];
   const T* dy = static_cast<const T*>(p.dy) + k.at(p.dys, b) + (t0 + row) * p.dys[2];
   T* dx = static_cast<T*>(p.dx) + k.at(p.dxs, b) + (t0 + row) * p.dxs[2];
-  const int64_t mine = tokens > row ? (tokens - row + p.rows - 1) / p.rows : 0;
-  for (int64_t j = (mine + kAtOnce - 1) / kAtOnce * kAtOnce - kAtOnce; j >= 0; j -= kAtOnce) {
+  const int mine = tokens > row ? (tokens - row + p.rows - 1) / p.rows : 0;
+  const int64_t hop = p.rows * p.xs[2], dyhop = p.rows * p.dys[2], dxhop = p.rows * p.dxs[2];
+  x += (mine - 1) * hop;
+  dy += (mine - 1) * dyhop;
+  dx += (mine - 1) * dxhop;
+  for (int left = mine; left > 0; left -= kAtOnce) {
     X v[kAtOnce], d[kAtOnce];
 #pragma unroll
-    for (int e = 0; e < kAtOnce; ++e)
-      if (j + e < mine) {
-        v[e].load(x + (j + e) * p.rows * p.xs[2]);
-        d[e].load(dy + (j + e) * p.rows * p.dys[2]);
+    for (int e = 0; e < kAtOnce; ++e) {
+      if (e < left) {
+        v[e].load(x);
+        d[e].load(dy);
       }
+      x -= e < left ? hop : 0;
+      dy -= e < left ? dyhop : 0;
+    }
 #pragma unroll
-    for (int e = 0; e < kAtOnce; ++e)
-      if (j + e < mine) {
-        float f[V], g[V];
+    for (int e = 0; e < kAtOnce; ++e) {
+      if (e < left) {
+        P f[kPacks], g[kPacks];
         v[e].open(f);
         d[e].open(g);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float xhat = (f[i] - mean[i / Q]) * rstd[i / Q];
-          const float q = g[i] * act_grad<T, ACT>(fmaf(xhat, w[i], o[i])) * w[i];
-          f[i] = rstd[i / Q] * (q - m0[i / Q] - xhat * m1[i / Q]);
+        for (int i = 0; i < kPacks; ++i) {
+          const int s = i * P::N / kStep;
+          const P xhat = mul_(add_(f[i], q.mean[s]), q.rstd[s]);
+          const P dz = act_grad<T, ACT>(fma_(xhat, q.weight[i], q.bias[i]), g[i]);
+          f[i] = mul_(q.rstd[s], fma_(xhat, m1[s], fma_(dz, q.weight[i], m0[s])));
         }
         v[e].close(f);
-        v[e].store(dx + (j + e) * p.rows * p.dxs[2]);
+        v[e].store(dx);
       }
+      dx -= dxhop;
+    }
   }
 }
 
@@ -520,7 +595,8 @@ __global__ void __launch_bounds__(kThreads) norm_small_kernel(const __grid_const
     for (int t = row; t < N; t += p.rows) {
       float f[V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) f[e] = act<T, ACT>(fmaf(values[t * p.n + i + e] - centre, scale[e], shift[e]));
+      for (int e = 0; e < V; ++e)
+        f[e] = act<T, ACT>(One{fmaf(values[t * p.n + i + e] - centre, scale[e], shift[e])}).v;
       X v;
       v.close(f);
       v.store(y + t * p.ys[2] + i);
@@ -564,7 +640,7 @@ __global__ void __launch_bounds__(kThreads) norm_small_grad_kernel(const __grid_
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           const float xhat = (f[e] - m.x) * m.y;
-          const float dz = h[e] * act_grad<T, ACT>(fmaf(xhat, w[e], o[e]));
+          const float dz = act_grad<T, ACT>(One{fmaf(xhat, w[e], o[e])}, One{h[e]}).v;
           values[t * p.n + i + e] = xhat;
           dzs[t * p.n + i + e] = dz;
           s0[e] += dz;
@@ -582,7 +658,7 @@ __global__ void __launch_bounds__(kThreads) norm_small_grad_kernel(const __grid_
   for (int c = threadIdx.x; c < p.n; c += kThreads) {
     float2 s = sums[c];
     for (int r = 1; r < p.rows; ++r) s.x += sums[r * p.n + c].x, s.y += sums[r * p.n + c].y;
-    reinterpret_cast<float2*>(p.part_sums)[int64_t(b) * p.C + g * p.n + c] = s;
+    p.channel_sums[int64_t(b) * p.C + g * p.n + c] = s;
   }
   const float count = float(N) * float(p.n), m0 = q.x / count, m1 = q.y / count;
   if (here)
@@ -606,7 +682,7 @@ __global__ void __launch_bounds__(kThreads) norm_small_grad_kernel(const __grid_
 struct Cut {
   bool small;
   int lanes, rows, col_blocks, row_blocks, slots, smem;
-  int64_t range;
+  int32_t range;
 };
 constexpr int kSmallBytes = 96 * 1024;        // of a group in shared memory, as fp32
 constexpr int64_t kSmallTotal = 1 << 21;      // values in all, above which SMs are full either way
@@ -630,23 +706,23 @@ bool fits_small(int32_t B, int64_t N, int C, int n, bool backward) {
   const int64_t bytes = N * n * (backward ? 8 : 4) + (backward ? int64_t(std::max(n, kThreads)) * 8 * 8 : 0);
   return B * N * C <= kSmallTotal && bytes <= kSmallBytes;
 }
-Cut cut_blocks(int32_t B, int64_t N, int C, int G, int V) {
+Cut cut_blocks(int32_t B, int64_t N, int C, int G, int V, bool backward) {
   Cut k{};
   const int vectors = C / V;
   k.col_blocks = (vectors + kThreads - 1) / kThreads;
   share(k, (vectors + k.col_blocks - 1) / k.col_blocks);
   k.slots = std::min(G, k.lanes * V / (C / G) + 2);
-  // four blocks an SM in all, of at least 32 tokens a thread
-  const int64_t most = std::max<int64_t>(1, 4 * 148 / (int64_t(B) * k.col_blocks));
-  const int64_t blocks = std::min<int64_t>(most, (N + k.rows * kRun - 1) / (k.rows * kRun));
-  k.range = (N + blocks - 1) / blocks;
+  // as many blocks as run at once (three an SM forward, two backward), of 8 tokens a thread or more
+  const int64_t most = std::max<int64_t>(1, (backward ? 2 : 3) * 148 / (int64_t(B) * k.col_blocks));
+  const int64_t blocks = std::min<int64_t>(most, (N + k.rows * 8 - 1) / (k.rows * 8));
+  k.range = int32_t((N + blocks - 1) / blocks);
   k.row_blocks = int((N + k.range - 1) / k.range);
   k.smem = k.rows * k.lanes * V * 8;
   return k;
 }
 size_t workspace_of(const Cut& k, int32_t B, int C, bool backward) {
-  if (!backward) return k.small ? 0 : size_t(B) * k.row_blocks * k.col_blocks * k.slots * 8;
-  return size_t(B) * k.row_blocks * C * 8 + size_t(B) * C * 8;
+  return (k.small ? 0 : size_t(B) * k.row_blocks * k.col_blocks * k.slots * 8) +
+         (backward ? size_t(B) * k.row_blocks * C * 8 : 0);
 }
 
 void put_cut(NormArgs& a, const Cut& k) {
@@ -667,7 +743,7 @@ int launch_small(bool backward, NormArgs& a, const Cut& k, cudaStream_t st) {
   const auto f = backward ? norm_small_grad_kernel<T, BYTES, ACT> : norm_small_kernel<T, BYTES, ACT>;
   if (!allow_smem(f, once[backward])) return TTT_ERR_CUDA;
   f<<<dim3(a.G, a.B), kThreads, k.smem, st>>>(a);
-  if (backward && (a.dweight || a.dbias)) norm_join_sums_kernel<<<(a.C + 31) / 32, 1024, 0, st>>>(a);
+  if (backward && (a.dweight || a.dbias)) norm_dweight_kernel<<<(a.C + 31) / 32, 1024, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
 }
 template <class T, int BYTES, int Q, int ACT>
@@ -675,8 +751,8 @@ int launch_blocks(bool backward, NormArgs& a, const Cut& k, cudaStream_t st) {
   const dim3 grid(k.col_blocks, k.row_blocks, a.B);
   if (backward) {
     norm_sums_kernel<T, BYTES, Q, ACT><<<grid, kThreads, k.smem, st>>>(a);
-    norm_join_sums_kernel<<<(a.C + 31) / 32, 1024, 0, st>>>(a);
     norm_dx_kernel<T, BYTES, Q, ACT><<<grid, kThreads, k.slots * 8, st>>>(a);
+    if (a.dweight || a.dbias) norm_dweight_kernel<<<(a.C + 31) / 32, 1024, 0, st>>>(a);
   } else {
     norm_parts_kernel<T, BYTES, Q><<<grid, kThreads, k.smem, st>>>(a);
     norm_apply_kernel<T, BYTES, Q, ACT><<<grid, kThreads, k.slots * 8, st>>>(a);
@@ -766,7 +842,7 @@ size_t space_needed(const ttt_norm* h, int32_t B, int64_t N, bool backward) {
   size_t most = 0;
   for (int wide : {16, 4, elem})
     if (c.C * elem % wide == 0)
-      most = std::max(most, workspace_of(cut_blocks(B, N, c.C, c.groups, wide / elem), B, c.C, backward));
+      most = std::max(most, workspace_of(cut_blocks(B, N, c.C, c.groups, wide / elem, backward), B, c.C, backward));
   return most;
 }
 
@@ -778,14 +854,10 @@ int run(const ttt_norm* h, bool backward, NormArgs& a, const RowTensor* t, const
   const int elem = c.dtype == TTT_BF16 ? 2 : 4;
   const bool small = fits_small(a.B, a.N, c.C, a.n, backward);
   const int wide = vector_bytes(t, nt, s, c.C, a.n, elem, small);
-  const Cut k = small ? cut_small(a.N, a.n, wide / elem, backward) : cut_blocks(a.B, a.N, c.C, c.groups, wide / elem);
+  const Cut k = small ? cut_small(a.N, a.n, wide / elem, backward) : cut_blocks(a.B, a.N, c.C, c.groups, wide / elem, backward);
   put_cut(a, k);
-  if (backward) {
-    a.part_sums = static_cast<float*>(workspace);
-    a.sums = a.part_sums + size_t(a.B) * k.row_blocks * c.C * 2;
-  } else {
-    a.parts = static_cast<float2*>(workspace);
-  }
+  a.channel_sums = static_cast<float2*>(workspace);
+  a.parts = a.channel_sums + (backward ? size_t(a.B) * k.row_blocks * c.C : 0);
   if (elem == 2)
     return wide == 16  ? launch<__nv_bfloat16, 16>(backward, c.act, a, k, st)
            : wide == 4 ? launch<__nv_bfloat16, 4>(backward, c.act, a, k, st)

@@ -40,6 +40,7 @@
 #include "ptx.cuh"
 #include "tc_gemm.cuh"
 #include "ttt_plan.cuh"
+#include "vec.cuh"
 
 namespace ttt {
 namespace {
@@ -75,42 +76,7 @@ struct ScanArgs {
   int32_t kept;           // kept states of a sequence
 };
 
-// The values of a lane's 4 bytes: one fp32 or two bf16, these in the packed fp32
-// arithmetic of sm_100 (one instruction for both).
-struct One {
-  float v;
-  __device__ __forceinline__ float operator[](int) const { return v; }
-};
-struct Two {
-  uint64_t w;
-  __device__ __forceinline__ float operator[](int i) const { return __uint_as_float(uint32_t(i ? w >> 32 : w)); }
-};
-__device__ __forceinline__ Two two(float a, float b) {
-  Two r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.w) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ One fma_(One a, One b, One c) { return {fmaf(a.v, b.v, c.v)}; }
-__device__ __forceinline__ One mul_(One a, One b) { return {a.v * b.v}; }
-__device__ __forceinline__ One add_(One a, One b) { return {a.v + b.v}; }
-__device__ __forceinline__ One sub_(One a, One b) { return {a.v - b.v}; }
-__device__ __forceinline__ Two fma_(Two a, Two b, Two c) {
-  Two r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.w) : "l"(a.w), "l"(b.w), "l"(c.w));
-  return r;
-}
-__device__ __forceinline__ Two mul_(Two a, Two b) {
-  Two r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.w) : "l"(a.w), "l"(b.w));
-  return r;
-}
-__device__ __forceinline__ Two add_(Two a, Two b) {
-  Two r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.w) : "l"(a.w), "l"(b.w));
-  return r;
-}
-__device__ __forceinline__ Two sub_(Two a, Two b) { return fma_(b, two(-1.f, -1.f), a); }
-
+// The values of a lane's 4 bytes: one fp32 or two bf16.
 template <class T>
 struct Word;
 template <>
@@ -136,17 +102,6 @@ struct Word<__nv_bfloat16> {
     return *reinterpret_cast<const uint32_t*>(&p);
   }
 };
-
-__device__ __forceinline__ float exp2_fast(float v) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-__device__ __forceinline__ float rcp_fast(float v) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
 
 // a and 1 - a of a lane's values; the complement is formed on its own, so that it keeps
 // its digits where a is close to 1.  bf16 inputs take the hardware's exponential (2^-22
