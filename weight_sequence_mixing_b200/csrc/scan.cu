@@ -45,10 +45,10 @@
 namespace ttt {
 namespace {
 
-constexpr int kWarps = 8;          // warps that sweep a tile's rows
-constexpr int kChainWarp = 8;      // two warps that follow the chain of states, tile about
-constexpr int kFeedWarp = 10;      // the warp that fetches rows
-constexpr int kThreads = 32 * 11;
+constexpr int kWarps = 16;             // warps that sweep a tile's rows
+constexpr int kChainWarp = kWarps;     // two warps that follow the chain of states, tile about
+constexpr int kFeedWarp = kWarps + 2;  // the warp that fetches rows
+constexpr int kThreads = 32 * (kWarps + 3);
 constexpr int kRowBytes = 128;     // a tile's channels: 32 lanes of 4 bytes
 constexpr int kSave = 64;          // tokens from one kept state to the next
 constexpr int kShort = 16;         // longest sequence of the short form
@@ -361,7 +361,7 @@ __device__ __forceinline__ void fetch(const ScanArgs& p, const void* base, const
 }
 
 template <class T, int GATE, int INPUT, bool BACKWARD>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
     scan_tile_kernel(const __grid_constant__ ScanArgs p, const __grid_constant__ CUtensorMap mg,
                      const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap md) {
   using S = Shape<T, BACKWARD>;
@@ -505,24 +505,20 @@ __global__ void __launch_bounds__(kThreads, 2)
       } else if (!wait(&sc.mapped[par], k / 2)) {
         return;
       }
-      float wa[kWarps][N], wh[kWarps][N];  // the warps' maps, in the order of the chain
+      // the tile's map: the warps' maps in the order of the chain
+      const float(*const mapA)[32 * N] = sc.A[par];
+      float(*const mapH)[32 * N] = BACKWARD ? sc.R[BACKWARD ? par : 0] : sc.H[par];
+#pragma unroll
+      for (int v = 0; v < N; ++v) A[v] = 1.f, H[v] = 0.f;
 #pragma unroll
       for (int j = 0; j < kWarps; ++j)
 #pragma unroll
         for (int v = 0; v < N; ++v) {
           const int w = BACKWARD ? kWarps - 1 - j : j;
-          wa[j][v] = sc.A[par][w][lane * N + v];
-          wh[j][v] = BACKWARD ? sc.R[par][w][lane * N + v] : sc.H[par][w][lane * N + v];
+          const float a = mapA[w][lane * N + v];
+          H[v] = apply(a, mapH[w][lane * N + v], H[v]);
+          A[v] *= a;
         }
-#pragma unroll
-      for (int v = 0; v < N; ++v) {
-        A[v] = 1.f, H[v] = 0.f;
-#pragma unroll
-        for (int j = 0; j < kWarps; ++j) {
-          H[v] = apply(wa[j][v], wh[j][v], H[v]);
-          A[v] *= wa[j][v];
-        }
-      }
       if (before > 0) {
         if (wanted) publish_map<N>(p, t, A, H);
         look_back<N>(p, t, before, step, st);
@@ -536,14 +532,12 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int w = BACKWARD ? kWarps - 1 - j : j;
 #pragma unroll
         for (int v = 0; v < N; ++v) {
-          if (BACKWARD)
-            sc.R[par][w][lane * N + v] = st[v];
-          else
-            sc.H[par][w][lane * N + v] = st[v];
+          const float h = mapH[w][lane * N + v];
+          mapH[w][lane * N + v] = st[v];
           if (!BACKWARD && w * kRows % kSave == 0 && p.saved && c + v < p.D &&
               int64_t(at.i) * kTile + w * kRows < len)
             p.saved[(int64_t(at.b) * p.kept + at.i * (kTile / kSave) + w * kRows / kSave) * p.D + c + v] = st[v];
-          st[v] = apply(wa[j][v], wh[j][v], st[v]);
+          st[v] = apply(mapA[w][lane * N + v], h, st[v]);
         }
       }
       __syncwarp();
@@ -787,7 +781,7 @@ int launch(ScanArgs& a, const int64_t (*strides)[2], cudaStream_t st) {
       if (!make_tmap(&m[k], base[k], int(sizeof(T)), a.D, a.L, a.B, strides[k][1], a.B > 1 ? strides[k][0] : 16, S::kTile))
         a.load = kLoad4;  // rows that TMA takes are on 4 bytes too
   }
-  const int grid = std::min(2 * sm_count(), a.total);
+  const int grid = std::min(sm_count(), a.total);
   // all ones: nothing published, and a counter whose first answer is -1
   if (a.counter && cudaMemsetAsync(a.counter, 0xff, space_of(a.total, S::N).total, st) != cudaSuccess)
     return TTT_ERR_CUDA;
