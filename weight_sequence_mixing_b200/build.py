@@ -12,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -47,17 +48,27 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     nvcc = nvcc_path()
     flags = NVCC_FLAGS + list(extra_flags or [])
     os.makedirs(BUILD, exist_ok=True)
-    objs, changed = [], False
+    objs, todo = [], []
     for src in sorted(glob.glob(os.path.join(CSRC, "*.cu"))):
         name = os.path.splitext(os.path.basename(src))[0]
         obj = os.path.join(BUILD, f"{name}.{_digest(src, flags)}.o")
         if not os.path.exists(obj):
-            cmd = [nvcc] + flags + ["-c", src, "-o", obj]
-            if verbose:
-                print(" ".join(cmd), file=sys.stderr)
-            subprocess.run(cmd, check=True)
-            changed = True
+            todo.append([nvcc] + flags + ["-c", src, "-o", obj])
         objs.append(obj)
+    changed = bool(todo)
+
+    def compile_one(cmd):
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        try:
+            subprocess.run(cmd, check=True)
+        except BaseException:
+            if os.path.exists(cmd[-1]):
+                os.remove(cmd[-1])  # a part of an object is not one
+            raise
+
+    with ThreadPoolExecutor(max_workers=os.cpu_count() or 1) as pool:
+        list(pool.map(compile_one, todo))
     # the objects the library was last linked from: relink whenever they differ (a
     # source reverted to an earlier version finds its old object in the cache)
     manifest = os.path.join(BUILD, "libttt_b200.objects")

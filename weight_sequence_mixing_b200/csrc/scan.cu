@@ -47,8 +47,9 @@ namespace {
 
 constexpr int kWarps = 16;             // warps that sweep a tile's rows
 constexpr int kChainWarp = kWarps;     // two warps that follow the chain of states, tile about
-constexpr int kFeedWarp = kWarps + 2;  // the warp that fetches rows
-constexpr int kThreads = 32 * (kWarps + 3);
+constexpr int kFeedWarp = kWarps + 2;  // the warp that fetches rows; without TMA the first of four
+constexpr int kFeeders = 4;
+constexpr int threads_of(bool tma) { return 32 * (kFeedWarp + (tma ? 1 : kFeeders)); }
 constexpr int kRowBytes = 128;     // a tile's channels: 32 lanes of 4 bytes
 constexpr int kSave = 64;          // tokens from one kept state to the next
 constexpr int kShort = 16;         // longest sequence of the short form
@@ -321,6 +322,7 @@ struct Shape {
     float H[2][kWarps][32 * N];   // and H, then in its place the state that enters the warp's rows
     float R[BACKWARD ? 2 : 1][BACKWARD ? kWarps : 1][32 * N];  // backward: the map A mu + R, then the mu that enters
     uint64_t full[kStages], empty[kStages];  // a stage's rows are there; are done with
+    uint64_t posted[kStages];                // a stage's tile is known to the feeders
     uint64_t mapped[2], entered[2];          // a tile's maps are there; its states
     Job job[kStages];                        // the stages' tiles
     int abort;
@@ -328,18 +330,18 @@ struct Shape {
   static constexpr int kSmem = 1024 + kStages * kStageBytes + int(sizeof(Scratch));
 };
 
-// One tensor's rows of a tile into shared memory, at the swizzle TMA uses, by one warp.
-// Nothing is read where the size is 0: the word is filled with zero.
-template <class T, int TILE>
+// A feeder's share of one tensor's rows of a tile, from token t0 on, into shared memory at the
+// swizzle TMA uses.  Nothing is read where the size is 0: the word is filled with zero.
+template <class T, int ROWS>
 __device__ __forceinline__ void fetch(const ScanArgs& p, const void* base, const int64_t (&s)[2], int b, int c, int64_t t0,
                                       int64_t len, uint8_t* dst) {
   const int lane = threadIdx.x % 32;
-  const int rows = c < p.D ? int(len - t0 < TILE ? len - t0 : TILE) : 0;
+  const int rows = c < p.D ? int(len - t0 >= ROWS ? ROWS : len > t0 ? len - t0 : 0) : 0;
   const T* from = static_cast<const T*>(base) + (rows ? b * s[0] + t0 * s[1] + c : 0);
   const uint32_t to = smem_u32(dst);
   if (p.load == kLoad4) {
 #pragma unroll 16
-    for (int r = 0; r < TILE; ++r) {
+    for (int r = 0; r < ROWS; ++r) {
       asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + r * kRowBytes + ((lane * 4) ^ ((r & 7) << 4))),
                    "l"(from), "r"(r < rows ? 4 : 0)
                    : "memory");
@@ -347,7 +349,7 @@ __device__ __forceinline__ void fetch(const ScanArgs& p, const void* base, const
     }
   } else {
 #pragma unroll 16
-    for (int r = 0; r < TILE; ++r) {
+    for (int r = 0; r < ROWS; ++r) {
       uint32_t w = 0;
       if (r < rows) {
         const uint16_t* h = reinterpret_cast<const uint16_t*>(from);
@@ -360,8 +362,8 @@ __device__ __forceinline__ void fetch(const ScanArgs& p, const void* base, const
   }
 }
 
-template <class T, int GATE, int INPUT, bool BACKWARD>
-__global__ void __launch_bounds__(kThreads, 1)
+template <class T, int GATE, int INPUT, bool BACKWARD, bool TMA>
+__global__ void __launch_bounds__(threads_of(TMA), 1)
     scan_tile_kernel(const __grid_constant__ ScanArgs p, const __grid_constant__ CUtensorMap mg,
                      const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap md) {
   using S = Shape<T, BACKWARD>;
@@ -376,7 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sc.full[s], p.load == kLoadTma ? 1 : 32);
+      mbar_init(&sc.full[s], TMA ? 1 : 32 * kFeeders);
+      mbar_init(&sc.posted[s], 1);
       mbar_init(&sc.empty[s], kWarps);
     }
     for (int s = 0; s < 2; ++s) {
@@ -395,6 +398,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     return __all_sync(~0u, ok) != 0;
   };
 
+  // this feeder's share of the rows of a stage's tile, without TMA
+  auto feed = [&](int s, const Job& job) {
+    constexpr int kShare = kTile / kFeeders;
+    if (job.t >= 0) {
+      const int f = (warp - kFeedWarp) * kShare, c = (job.at.col * 32 + lane) * N;
+      const int64_t t0 = int64_t(job.at.i) * kTile + f;
+      uint8_t* const to = stages + s * S::kStageBytes + f * kRowBytes;
+      fetch<T, kShare>(p, p.g, p.gs, job.at.b, c, t0, job.len, to);
+      fetch<T, kShare>(p, p.x, p.xs, job.at.b, c, t0, job.len, to + S::kBox);
+      if (BACKWARD) fetch<T, kShare>(p, p.dh, p.dhs, job.at.b, c, t0, job.len, to + 2 * S::kBox);
+    }
+    if (p.load == kLoad4)  // arrives when this lane's copies have
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sc.full[s])) : "memory");
+    else
+      mbar_arrive(&sc.full[s]);
+  };
+  if (!TMA && warp > kFeedWarp) {  // the first feeder's helpers
+    for (int k = 0, ends = 0; ends < 2; ++k) {
+      const int s = k % kStages;
+      if (!wait(&sc.posted[s], k / kStages)) break;
+      const Job job = sc.job[s];
+      feed(s, job);
+      ends += job.t < 0;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
+  }
   if (warp == kFeedWarp) {
     auto hand_out = [&](int turn) {
       int t = 0;
@@ -430,12 +460,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int s = k % kStages;
       if (k >= kStages && !wait(&sc.empty[s], k / kStages - 1)) break;
-      if (lane == 0) sc.job[s] = Job{more ? t : -1, int(len), at};
+      const Job job{more ? t : -1, int(len), at};
+      if (lane == 0) sc.job[s] = job;
       __syncwarp();
-      uint8_t* const to = stages + s * S::kStageBytes;
-      const int c0 = at.col * 32 * N;
-      if (p.load == kLoadTma) {
+      if constexpr (TMA) {
         if (lane == 0) {
+          uint8_t* const to = stages + s * S::kStageBytes;
+          const int c0 = at.col * 32 * N;
           if (more) {
             mbar_arrive_expect_tx(&sc.full[s], S::kStageBytes);
             tma_load_3d(to, &mg, &sc.full[s], c0, int(t0), at.b);
@@ -446,15 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else {
-        if (more) {
-          fetch<T, kTile>(p, p.g, p.gs, at.b, c0 + lane * N, t0, len, to);
-          fetch<T, kTile>(p, p.x, p.xs, at.b, c0 + lane * N, t0, len, to + S::kBox);
-          if (BACKWARD) fetch<T, kTile>(p, p.dh, p.dhs, at.b, c0 + lane * N, t0, len, to + 2 * S::kBox);
-        }
-        if (p.load == kLoad4)  // arrives when this lane's copies have
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sc.full[s])) : "memory");
-        else
-          mbar_arrive(&sc.full[s]);
+        if (lane == 0) mbar_arrive(&sc.posted[s]);
+        feed(s, job);
       }
       ++k;
     }
@@ -767,13 +791,6 @@ int launch(ScanArgs& a, const int64_t (*strides)[2], cudaStream_t st) {
     scan_short_kernel<T, GATE, INPUT, BACKWARD><<<unsigned(grid), 128, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
   }
-  const auto kernel = scan_tile_kernel<T, GATE, INPUT, BACKWARD>;
-  static OncePerDevice once;
-  const int dev = current_device();
-  if (once.run(dev, [&] {
-        return int(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem));
-      }) != 0)
-    return TTT_ERR_CUDA;
   CUtensorMap m[3] = {};
   if (a.load == kLoadTma) {
     const void* base[3] = {a.g, a.x, a.dh};
@@ -781,11 +798,19 @@ int launch(ScanArgs& a, const int64_t (*strides)[2], cudaStream_t st) {
       if (!make_tmap(&m[k], base[k], int(sizeof(T)), a.D, a.L, a.B, strides[k][1], a.B > 1 ? strides[k][0] : 16, S::kTile))
         a.load = kLoad4;  // rows that TMA takes are on 4 bytes too
   }
+  const bool tma = a.load == kLoadTma;
+  const auto kernel = tma ? scan_tile_kernel<T, GATE, INPUT, BACKWARD, true> : scan_tile_kernel<T, GATE, INPUT, BACKWARD, false>;
+  static OncePerDevice once[2];
+  const int dev = current_device();
+  if (once[tma].run(dev, [&] {
+        return int(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem));
+      }) != 0)
+    return TTT_ERR_CUDA;
   const int grid = std::min(sm_count(), a.total);
   // all ones: nothing published, and a counter whose first answer is -1
   if (a.counter && cudaMemsetAsync(a.counter, 0xff, space_of(a.total, S::N).total, st) != cudaSuccess)
     return TTT_ERR_CUDA;
-  kernel<<<grid, kThreads, S::kSmem, st>>>(a, m[0], m[1], m[2]);
+  kernel<<<grid, threads_of(tma), S::kSmem, st>>>(a, m[0], m[1], m[2]);
   return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
 }
 
