@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_parts_kernel(const __grid_co
   using P = typename X::P;
   constexpr int V = X::N, K = V / Q, kPacks = X::kPacks, kSums = Q > 1 ? K : kPacks, kAtOnce = 8;
   extern __shared__ float2 threads[];  // [row][sum of the block]
+  cudaTriggerProgrammaticLaunchCompletion();  // the next kernel's blocks may take the places that fall free
   const int cb = blockIdx.x, rb = blockIdx.y, b = blockIdx.z;
   const Column k = column(p, cb, V);
   const int row = threadIdx.x / p.lanes;
@@ -246,6 +247,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_apply_kernel(const __grid_co
   const Column k = column(p, cb, V);
   const int row = threadIdx.x / p.lanes;
   const int c0 = cb * p.lanes * V, c1 = block_end(p, cb, V), g0 = c0 / p.n;
+  cudaGridDependencySynchronize();  // the parts are there
   for (int g = g0 + threadIdx.x / 32; g <= (c1 - 1) / p.n; g += kThreads / 32) {
     const float2 m = join_parts(p, b, g, V);
     if (threadIdx.x % 32 == 0) {
@@ -338,6 +340,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_sums_kernel(const __grid_con
   using P = typename X::P;
   constexpr int V = X::N, kPacks = X::kPacks, kStep = Q > P::N ? Q : P::N, kMeans = V / kStep, kAtOnce = 4;
   extern __shared__ float2 threads[];
+  cudaTriggerProgrammaticLaunchCompletion();
   const int cb = blockIdx.x, rb = blockIdx.y, b = blockIdx.z;
   const Column k = column(p, cb, V);
   const int row = threadIdx.x / p.lanes;
@@ -425,6 +428,7 @@ __global__ void __launch_bounds__(1024) norm_dweight_kernel(const __grid_constan
   __shared__ float2 rows[32][32];
   const int c = blockIdx.x * 32 + threadIdx.x % 32, r = threadIdx.x / 32;
   const int64_t all = int64_t(p.B) * p.row_blocks;
+  cudaGridDependencySynchronize();
   float2 s = make_float2(0.f, 0.f);
   if (c < p.C)
     for (int64_t q = r; q < all; q += 32) {
@@ -454,6 +458,8 @@ __global__ void __launch_bounds__(kThreads, 2) norm_dx_kernel(const __grid_const
   const int row = threadIdx.x / p.lanes;
   const int c0 = cb * p.lanes * V, c1 = block_end(p, cb, V), g0 = c0 / p.n;
   const float inv = 1.f / (float(p.N) * float(p.n));
+  cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();  // the sums are there
   for (int g = g0 + threadIdx.x / 32; g <= (c1 - 1) / p.n; g += kThreads / 32) {
     const int width = p.lanes * V, first = g * p.n / width, blocks = ((g + 1) * p.n - 1) / width - first + 1;
     float q0 = 0.f, q1 = 0.f;
@@ -737,13 +743,30 @@ bool allow_smem(F* kernel, OncePerDevice& once) {
          }) == 0;
 }
 
+// A launch whose blocks may start while the kernel before it ends; the kernel itself waits
+// for that one's results (cudaGridDependencySynchronize).
+template <class F>
+void launch_behind(F* kernel, dim3 grid, int threads, int smem, const NormArgs& a, cudaStream_t st) {
+  cudaLaunchAttribute behind;
+  behind.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  behind.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  c.attrs = &behind;
+  c.numAttrs = 1;
+  cudaLaunchKernelEx(&c, kernel, a);
+}
+
 template <class T, int BYTES, int ACT>
 int launch_small(bool backward, NormArgs& a, const Cut& k, cudaStream_t st) {
   static OncePerDevice once[2];
   const auto f = backward ? norm_small_grad_kernel<T, BYTES, ACT> : norm_small_kernel<T, BYTES, ACT>;
   if (!allow_smem(f, once[backward])) return TTT_ERR_CUDA;
   f<<<dim3(a.G, a.B), kThreads, k.smem, st>>>(a);
-  if (backward && (a.dweight || a.dbias)) norm_dweight_kernel<<<(a.C + 31) / 32, 1024, 0, st>>>(a);
+  if (backward && (a.dweight || a.dbias)) launch_behind(norm_dweight_kernel, dim3((a.C + 31) / 32), 1024, 0, a, st);
   return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
 }
 template <class T, int BYTES, int Q, int ACT>
@@ -751,11 +774,11 @@ int launch_blocks(bool backward, NormArgs& a, const Cut& k, cudaStream_t st) {
   const dim3 grid(k.col_blocks, k.row_blocks, a.B);
   if (backward) {
     norm_sums_kernel<T, BYTES, Q, ACT><<<grid, kThreads, k.smem, st>>>(a);
-    norm_dx_kernel<T, BYTES, Q, ACT><<<grid, kThreads, k.slots * 8, st>>>(a);
-    if (a.dweight || a.dbias) norm_dweight_kernel<<<(a.C + 31) / 32, 1024, 0, st>>>(a);
+    launch_behind(norm_dx_kernel<T, BYTES, Q, ACT>, grid, kThreads, k.slots * 8, a, st);
+    if (a.dweight || a.dbias) launch_behind(norm_dweight_kernel, dim3((a.C + 31) / 32), 1024, 0, a, st);
   } else {
     norm_parts_kernel<T, BYTES, Q><<<grid, kThreads, k.smem, st>>>(a);
-    norm_apply_kernel<T, BYTES, Q, ACT><<<grid, kThreads, k.slots * 8, st>>>(a);
+    launch_behind(norm_apply_kernel<T, BYTES, Q, ACT>, grid, kThreads, k.slots * 8, a, st);
   }
   return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
 }
