@@ -26,7 +26,7 @@ namespace ttt {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRun = 32;  // tokens summed about one value
+constexpr int kRun = 32;  // tokens summed about one value; a multiple of the loads under way
 
 struct NormArgs {
   const void *x, *dy;
@@ -143,31 +143,36 @@ __global__ void __launch_bounds__(kThreads, 3) norm_parts_kernel(const __grid_co
     const T* x = static_cast<const T*>(p.x) + k.at(p.xs, b) + (t0 + row) * p.xs[2];
     const int64_t hop = p.rows * p.xs[2];
     float count = 0.f, mean[K] = {}, S[K] = {};
-    for (int left = tokens > row ? (tokens - row + p.rows - 1) / p.rows : 0; left > 0;) {
+    int left = tokens > row ? (tokens - row + p.rows - 1) / p.rows : 0;
+    X v[kAtOnce];  // each place takes the vector kAtOnce rows on as soon as it is free
+#pragma unroll
+    for (int e = 0; e < kAtOnce; ++e) {
+      if (e < left) v[e].load(x);
+      x += e < left ? hop : 0;
+    }
+    while (left > 0) {
       const int run = min(left, kRun);
       P off[kPacks], s[kSums], q[kSums];  // off: less the run's first value; a pack's sums side by side
+      {
+        float f[V];
+        v[0].open(f);
+#pragma unroll
+        for (int i = V - 1; i >= 0; --i) f[i] = -f[Q > 1 ? i / Q * Q : i];  // a sum's first is the last to change
+#pragma unroll
+        for (int i = 0; i < kPacks; ++i) off[i] = P::of(f + i * P::N);
+#pragma unroll
+        for (int i = 0; i < kSums; ++i) s[i] = P::all(0.f), q[i] = P::all(0.f);
+      }
       for (int j = 0; j < run; j += kAtOnce) {
-        X v[kAtOnce];
-#pragma unroll
-        for (int e = 0; e < kAtOnce; ++e) {
-          if (j + e < run) v[e].load(x);
-          x += j + e < run ? hop : 0;
-        }
-        if (j == 0) {
-          float f[V];
-          v[0].open(f);
-#pragma unroll
-          for (int i = V - 1; i >= 0; --i) f[i] = -f[Q > 1 ? i / Q * Q : i];  // a sum's first is the last to change
-#pragma unroll
-          for (int i = 0; i < kPacks; ++i) off[i] = P::of(f + i * P::N);
-#pragma unroll
-          for (int i = 0; i < kSums; ++i) s[i] = P::all(0.f), q[i] = P::all(0.f);
-        }
 #pragma unroll
         for (int e = 0; e < kAtOnce; ++e)
           if (j + e < run) {
             P f[kPacks];
             v[e].open(f);
+            if (j + e + kAtOnce < left) {
+              v[e].load(x);
+              x += hop;
+            }
 #pragma unroll
             for (int i = 0; i < kPacks; ++i) {
               const P d = add_(f[i], off[i]);
@@ -283,24 +288,28 @@ __global__ void __launch_bounds__(kThreads, 3) norm_apply_kernel(const __grid_co
   const int64_t hop = p.rows * p.xs[2], yhop = p.rows * p.ys[2];
   x += (mine - 1) * hop;
   y += (mine - 1) * yhop;
-  for (int left = mine; left > 0; left -= kAtOnce) {  // last to first
-    X v[kAtOnce];
+  X v[kAtOnce];  // last row to first, the loads kAtOnce rows ahead
+#pragma unroll
+  for (int e = 0; e < kAtOnce; ++e) {
+    if (e < mine) v[e].load(x);
+    x -= e < mine ? hop : 0;
+  }
+  for (int left = mine; left > 0; left -= kAtOnce) {
 #pragma unroll
     for (int e = 0; e < kAtOnce; ++e) {
-      if (e < left) v[e].load(x);
-      x -= e < left ? hop : 0;
-    }
-#pragma unroll
-    for (int e = 0; e < kAtOnce; ++e) {
-      if (e < left) {
-        P f[kPacks];
-        v[e].open(f);
-#pragma unroll
-        for (int i = 0; i < kPacks; ++i)
-          f[i] = act<T, ACT>(fma_(add_(f[i], mean[i * P::N / kStep]), scale[i], shift[i]));
-        v[e].close(f);
-        v[e].store(y);
+      if (e >= left) break;
+      P f[kPacks];
+      v[e].open(f);
+      if (e + kAtOnce < left) {
+        v[e].load(x);
+        x -= hop;
       }
+#pragma unroll
+      for (int i = 0; i < kPacks; ++i)
+        f[i] = act<T, ACT>(fma_(add_(f[i], mean[i * P::N / kStep]), scale[i], shift[i]));
+      X o;
+      o.close(f);
+      o.store(y);
       y -= yhop;
     }
   }
