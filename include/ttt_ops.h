@@ -126,6 +126,11 @@ int ttt_scan_backward(const ttt_scan* handle, int32_t B, int64_t L, const void* 
                       const ttt_strides* dgs, void* dx, const ttt_strides* dxs, float* dh0, void* workspace,
                       size_t workspace_bytes, unsigned* status, void* stream);
 
+/* Zeroes the rows of y [B, L, D] from each sequence's length on (lengths as above, not
+ * NULL): what forward and backward leave as it was, for a tensor that is new. */
+int ttt_scan_clear(const ttt_scan* handle, int32_t B, int64_t L, const int32_t* lengths, void* y,
+                   const ttt_strides* ys, void* stream);
+
 /* -------------------------------------------------- group norm with an activation
  * Channel c = k (C / groups) + i of group k; mean and variance (divided by n) over the
  * group's channels of all N tokens of a batch entry:

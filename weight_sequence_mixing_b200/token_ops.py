@@ -34,7 +34,6 @@ ACT = {"none": 0, "silu": 1, "gelu": 2}
 POS_DTYPE = {torch.int32: 0, torch.float32: 1}
 MAX_AXES = 4
 _STATUS_TIMEOUT = 2
-_SHORT_SCAN = 16  # tokens up to which a scan needs no workspace
 
 
 class RopeConfig(ctypes.Structure):
@@ -152,6 +151,20 @@ class _Op:
             return call(*args)
 
 
+class _Sizes(dict):
+    """Byte counts that depend on a call's sizes alone, asked of the library once for each."""
+
+    def __init__(self, ask):
+        super().__init__()
+        self._ask = ask
+
+    def __missing__(self, key):
+        if len(self) >= 4096:
+            self.clear()
+        n = self[key] = self._ask(*key)
+        return n
+
+
 class _StatusOp(_Op):
     """An operator whose kernels wait on one another and report a wait that ran out."""
 
@@ -248,6 +261,8 @@ class GatedScan(_StatusOp):
         k.D, k.gate, k.input, k.dtype = c["D"], GATE[c["gate"]], SCAN_INPUT[c["inp"]], DTYPE[c["dtype"]]
         self.D = int(c["D"])
         self._open(LIB.ttt_scan_create, LIB.ttt_scan_destroy, k)
+        self._space = _Sizes(lambda B, L: LIB.ttt_scan_workspace_size(self._handle, B, L))
+        self._saved = _Sizes(lambda B, L: LIB.ttt_scan_saved_size(self._handle, B, L))
 
     def _sizes(self, x, lengths):
         shape = x.shape
@@ -257,22 +272,24 @@ class GatedScan(_StatusOp):
             self._whole("lengths", lengths, (shape[0],), torch.int32)
         return (shape[0], shape[1], self.D), (shape[0], self.D)
 
-    def _saved_bytes(self, B, L):
-        return LIB.ttt_scan_saved_size(self._open_handle(), B, L)
-
     def _check_saved(self, saved, B, L):
-        n = self._saved_bytes(B, L)
+        n = self._saved[B, L]
         if saved.dtype != torch.uint8 or saved.numel() < n or not saved.is_contiguous() or \
                 saved.get_device() != self._index:
             raise ValueError(f"saved: expected at least {n} contiguous bytes on cuda:{self._index} (new_saved)")
 
     def new_saved(self, B: int, L: int, stream=None):
         """A buffer for what a forward call leaves for its backward call."""
-        return self._run(stream, (), self._bytes, max(16, self._saved_bytes(B, L)))
+        self._open_handle()
+        return self._run(stream, (), self._bytes, max(16, self._saved[B, L]))
 
-    def _new(self, x, shape, lengths):
-        # rows behind a sequence's end are left as they are: zeros, in a tensor made here
-        return _plain(x, shape, self.io_dtype) if lengths is None else x.new_zeros(shape, dtype=self.io_dtype)
+    def _new(self, handle, x, shape, lengths):
+        out = _plain(x, shape, self.io_dtype)
+        if lengths is not None:  # rows behind a sequence's end are left as they are: zeros, in a tensor made here
+            s = out.stride()
+            _check(LIB.ttt_scan_clear(handle, shape[0], shape[1], lengths.data_ptr(), out.data_ptr(),
+                                      _strides(s[0], 0, s[1]), _current_stream(self._index)), "ttt_scan_clear")
+        return out
 
     def forward(self, g, x, h0=None, lengths=None, saved=None, out=None, h_last=None, stream=None):
         """Returns (h [B, L, D], h_last [B, D]).  lengths: [B] int32, each sequence's own length; rows from
@@ -294,10 +311,10 @@ class GatedScan(_StatusOp):
     def _launch_forward(self, handle, g, x, h0, lengths, saved, out, h_last, shape, state):
         B, L, _ = shape
         if out is None:
-            out = self._new(x, shape, lengths)
+            out = self._new(handle, x, shape, lengths)
         if h_last is None:
             h_last = _plain(x if h0 is None else h0, state, torch.float32)
-        n = LIB.ttt_scan_workspace_size(handle, B, L) if L > _SHORT_SCAN else 0
+        n = self._space[B, L]
         ws = self._bytes(n)
         gs, xs, hs = g.stride(), x.stride(), out.stride()
         st = LIB.ttt_scan_forward(handle, B, L, g.data_ptr(), _strides(gs[0], 0, gs[1]), x.data_ptr(),
@@ -324,11 +341,11 @@ class GatedScan(_StatusOp):
 
     def _launch_backward(self, handle, dh, g, x, saved, dh_last, lengths, dg, dx, dh0, shape, state):
         B, L, _ = shape
-        dg = self._new(x, shape, lengths) if dg is None else dg
-        dx = self._new(x, shape, lengths) if dx is None else dx
+        dg = self._new(handle, x, shape, lengths) if dg is None else dg
+        dx = self._new(handle, x, shape, lengths) if dx is None else dx
         if dh0 is None:
             dh0 = _plain(x if dh_last is None else dh_last, state, torch.float32)
-        n = LIB.ttt_scan_workspace_size(handle, B, L) if L > _SHORT_SCAN else 0
+        n = self._space[B, L]
         ws = self._bytes(n)
         s = [_strides(t.stride(0), 0, t.stride(1)) for t in (dh, g, x, dg, dx)]
         st = LIB.ttt_scan_backward(handle, B, L, dh.data_ptr(), s[0], _ptr(dh_last), g.data_ptr(), s[1], x.data_ptr(),
@@ -352,6 +369,7 @@ class GroupNorm(_StatusOp):
         k.dtype = DTYPE[c["dtype"]]
         self._open(LIB.ttt_norm_create, LIB.ttt_norm_destroy, k)
         self.C, self.groups = int(c["C"]), int(c["groups"])
+        self._space = _Sizes(lambda B, N, backward: LIB.ttt_norm_workspace_size(self._handle, B, N, backward))
         self._each = self.C // self.groups  # channels of a group
 
     def new_stats(self, B: int, stream=None):
@@ -395,7 +413,7 @@ class GroupNorm(_StatusOp):
     def _launch_forward(self, handle, x, weight, bias, stats, out, rows):
         if out is None:
             out = _plain(x, rows, self.io_dtype)
-        n = LIB.ttt_norm_workspace_size(handle, rows[0], rows[1], 0)
+        n = self._space[rows[0], rows[1], 0]
         ws = self._bytes(n)
         st = LIB.ttt_norm_forward(handle, rows[0], rows[1], x.data_ptr(), self._strides(x), _ptr(weight), _ptr(bias),
                                   out.data_ptr(), self._strides(out), _ptr(stats), _ptr(ws), n, self._status_ptr,
@@ -425,7 +443,7 @@ class GroupNorm(_StatusOp):
             dweight = _plain(x if weight is None else weight, (self.C,), torch.float32)
         if dbias is None:
             dbias = _plain(x if bias is None else bias, (self.C,), torch.float32)
-        n = LIB.ttt_norm_workspace_size(handle, rows[0], rows[1], 1)
+        n = self._space[rows[0], rows[1], 1]
         ws = self._bytes(n)
         st = LIB.ttt_norm_backward(handle, rows[0], rows[1], dy.data_ptr(), self._strides(dy), x.data_ptr(),
                                    self._strides(x), _ptr(weight), _ptr(bias), stats.data_ptr(), dx.data_ptr(),
