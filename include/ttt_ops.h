@@ -26,9 +26,9 @@
  *     before a call do not matter, and calls whose GPU work overlaps need a
  *     workspace each (two captured graphs that replay at once among them).
  *   - `status` (optional, 4 bytes of device memory) collects the device status bits:
- *     a call that goes wrong on the device sets bits and writes NaN where its
- *     result is unknown; no call clears them.  Bit 1 (value 2): a bounded device
- *     wait ran out.
+ *     a call that goes wrong on the device sets bits, and its outputs are then not to
+ *     be used; no call clears them.  Bit 1 (value 2): a bounded device wait ran out
+ *     (2 s, as in ttt.h).
  *   - Results do not depend on timing: the same call gives the same bits.
  */
 #ifndef TTT_OPS_H_
@@ -86,7 +86,10 @@ int ttt_rope_apply(const ttt_rope* handle, int32_t B, int32_t H, int64_t N, cons
  * Backward, for the gradients dh of every h_t and dh_last of h_len:
  *   lam_t = dh_t + a_{t+1} lam_{t+1}  (lam_len = dh_len + dh_last)
  *   dx = lam | (1 - a) lam;  da = lam h_{t-1} | lam (h_{t-1} - x);  dg = da a'(g);  dh0 = a_1 lam_1
- * States and products are fp32; g, x, h, dh, dg, dx are in `dtype`. */
+ * States and products are fp32; g, x, h, dh, dg, dx are in `dtype`.  Products of the
+ * gates of up to 256 tokens in a row are formed: gates that grow a state (|a| > 1) have to
+ * keep them, and the states, within fp32's range; beyond it results are infinite or NaN,
+ * in their channel and batch entry alone. */
 typedef enum { TTT_GATE_VALUE = 0, TTT_GATE_SIGMOID = 1, TTT_GATE_EXP = 2 } ttt_gate_kind;
 typedef enum { TTT_SCAN_PLAIN = 0, TTT_SCAN_COMPLEMENT = 1 } ttt_scan_input;
 
@@ -157,7 +160,7 @@ int ttt_norm_create(const ttt_norm_config* cfg, ttt_norm** out);
 void ttt_norm_destroy(ttt_norm* handle);
 size_t ttt_norm_workspace_size(const ttt_norm* handle, int32_t B, int64_t N, int32_t backward);
 
-/* x, y: B >= 1, N >= 1 tokens of C channels.  weight, bias: [C] fp32 or NULL (one, zero).
+/* x, y: 1 <= B <= 65535, 1 <= N <= 2^30 tokens of C channels.  weight, bias: [C] fp32 or NULL (one, zero).
  * stats: [B, groups, 2] fp32 (mean, 1 / sqrt(var + eps)) for the backward call, or
  * NULL.  y may be x (same pointer and strides), which leaves no x for a backward call. */
 int ttt_norm_forward(const ttt_norm* handle, int32_t B, int64_t N, const void* x, const ttt_strides* xs,

@@ -120,6 +120,18 @@ def test_scan_forward_calls_that_are_refused(kw):
     binding.LIB.ttt_scan_destroy(h)
 
 
+def test_scan_clear_calls_that_are_refused():
+    binding, ops = _lib()
+    st, h = _open("scan", ops.ScanConfig(D=64, gate=1, input=1, dtype=1))
+    call = lambda B=2, L=700, n=97 * M, y=112 * M, s=(44800, 0, 64): binding.LIB.ttt_scan_clear(  # noqa: E731
+        h, B, L, n, y, _s(*s), None)
+    for bad in (dict(B=0), dict(L=-1), dict(n=None), dict(n=97 * M + 2), dict(y=None), dict(y=112 * M + 1),
+                dict(s=(44800, 0, 63)), dict(n=112 * M)):
+        assert call(**bad) == binding.TTT_ERR_INVALID_ARG, bad
+    assert call(L=(1 << 30) + 1) == binding.TTT_ERR_UNSUPPORTED
+    binding.LIB.ttt_scan_destroy(h)
+
+
 BWD_OK = dict(B=2, L=700, dh=64 * M, dh_last=98 * M, g=80 * M, x=96 * M + 4 * M, lengths=97 * M, saved=128 * M,
               dg=112 * M, dx=120 * M, dh0=99 * M, ws=160 * M, wsn=1 << 30, status=None,
               dhs=(44800, 0, 64), gs=(44800, 0, 64), xs=(44800, 0, 64), dgs=(44800, 0, 64), dxs=(44800, 0, 64))

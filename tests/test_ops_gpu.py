@@ -342,6 +342,72 @@ def _dot64(d, key, v):
     return (o[key] * v).sum()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,wide", [(70, 144), (72, 144), (33, 64), (1, 8), (9, 9)])
+def test_scan_rows_of_any_width_and_stride(dtype, D, wide):
+    """Channels that are no whole number of a tile's columns, in rows that start on 16 bytes, on 4 or on 2."""
+    case = (2, 600, D, "exp", "complement", dtype, True, True, False)
+    d = _scan_inputs(case)
+    for at in (0, wide - D):
+        strided = {}
+        for k in ("g", "x", "dh"):
+            rows = torch.full((2, 600, wide), math.nan, dtype=DT[dtype], device="cuda")
+            strided[k] = rows[..., at:at + D]
+            strided[k].copy_(d[k])
+        op = _ops().GatedScan(dict(D=D, gate="exp", inp="complement", dtype=dtype))
+        saved, n = op.new_saved(2, 600), d["lengths"].cuda()
+        out = [torch.full((2, 600, wide), 7.0, dtype=DT[dtype], device="cuda") for _ in range(3)]
+        h, dg, dx = (t[..., at:at + D] for t in out)
+        _, last = op.forward(strided["g"], strided["x"], h0=d["h0"].cuda(), lengths=n, saved=saved, out=h)
+        _, _, dh0 = op.backward(strided["dh"], strided["g"], strided["x"], saved, dh_last=d["dh_last"].cuda(), lengths=n,
+                                dg=dg, dx=dx)
+        op.check_status()
+        beside = torch.ones(wide, dtype=torch.bool)
+        beside[at:at + D] = False
+        assert all((t.cpu()[..., beside] == 7.0).all() for t in out)
+        behind = torch.arange(600)[None, :] >= d["lengths"][:, None]
+        for t in (h, dg, dx):
+            assert (t.cpu()[behind] == 7.0).all()
+            t[behind.cuda()] = 0.0
+        _check_scan(case, d, dict(h=h, h_last=last, dg=dg, dx=dx, dh0=dh0))
+
+
+def test_scans_on_two_streams_at_once_and_a_broadcast_input():
+    """Long chains of tiles on two streams side by side, the gates broadcast over the batch (stride 0)."""
+    op = _ops().GatedScan(dict(D=96, gate="sigmoid", inp="plain", dtype="bf16"))
+    gen = _gen(8)
+    g = (_randn(gen, 1, 20000, 96) + 3).bfloat16().cuda().expand(3, -1, -1)
+    x = _randn(gen, 3, 20000, 96).bfloat16().cuda()
+    want = op.forward(g.contiguous(), x)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[op.forward(g, x, stream=s) for _ in range(6)] for s in streams]
+    op.check_status()
+    for h, last in (r for rs in got for r in rs):
+        assert torch.equal(h, want[0]) and torch.equal(last, want[1])
+
+
+def test_many_short_sequences():
+    """More batch entries than a grid has rows: one new token and a few of each."""
+    B, D = 70001, 6
+    gen = _gen(12)
+    x = _randn(gen, B, 3, D).bfloat16()
+    op = _ops().GatedScan(dict(D=D, gate="value", inp="plain", dtype="bf16"))
+    g = torch.full_like(x, 0.5).cuda()
+    n = torch.arange(B, dtype=torch.int32) % 4
+    h, last = op.forward(g, x.cuda(), lengths=n.cuda())
+    want = torch.zeros(B, D)
+    for t in range(3):
+        want = torch.where((t < n)[:, None], 0.5 * want + x[:, t].float(), want)
+    assert torch.equal(last.cpu(), want)
+    assert (h.cpu()[torch.arange(3)[None] >= n[:, None]] == 0).all()
+    rope = _ops().RotaryPositions(dict(d=6, pairs=(3,), dtype="bf16"))
+    pos = torch.arange(3 * B, dtype=torch.int32).view(B, 3, 1)
+    y = rope.forward(x.view(B, 1, 3, D).cuda(), pos.cuda())
+    want, err = ref.rope(x.view(B, 1, 3, D).double(), pos, (3,), 10000.0, "halves")
+    ref.check("y", y, want, ref.rounded(want, err, torch.bfloat16))
+
+
 def test_scan_longer_than_32_bit_offsets():
     """A scan whose tensors hold more than 2^31 elements: its last rows."""
     L, D = (1 << 19) + 77, 4104

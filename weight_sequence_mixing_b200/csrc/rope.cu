@@ -8,6 +8,7 @@
 // position of 10^6 would lose three digits of the angle.)
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 #include <new>
 
 #include "op_checks.h"
@@ -20,8 +21,7 @@ namespace {
 constexpr long double kTwoPi = 6.283185307179586476925286766559L;
 
 struct RopeTable {
-  double turns[TTT_ROPE_MAX_PAIRS];      // theta_i / 2 pi
-  uint64_t fraction[TTT_ROPE_MAX_PAIRS]; // its fraction in units of 2^-64
+  uint64_t turns[TTT_ROPE_MAX_PAIRS];  // theta_i / 2 pi: its fraction in units of 2^-64, or (fp32 positions) an fp64's bits
   unsigned char axis[TTT_ROPE_MAX_PAIRS];
 };
 
@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(256, ONE ? 3 : 2)
   int axis[P];
 #pragma unroll
   for (int k = 0; k < P; ++k) {
-    freq[k] = POS_F32 ? uint64_t(__double_as_longlong(tab.turns[i0 + k])) : tab.fraction[i0 + k];
+    freq[k] = tab.turns[i0 + k];
     axis[k] = tab.axis[i0 + k];
     // held in registers: read again at each use, the lanes' different places in constant
     // memory come one after another (575 us for the views below)
@@ -203,7 +203,7 @@ using namespace ttt;
 struct ttt_rope {
   ttt_rope_config cfg;
   int32_t pairs;
-  RopeTable tab;
+  RopeTable tab[2];  // for int32 and for fp32 positions
 };
 
 extern "C" int ttt_rope_create(const ttt_rope_config* c, ttt_rope** out) {
@@ -227,9 +227,10 @@ extern "C" int ttt_rope_create(const ttt_rope_config* c, ttt_rope** out) {
   for (int a = 0; a < c->axes; ++a)
     for (int j = 0; j < c->pairs[a]; ++j, ++at) {
       const long double turns = powl(c->base[a], -static_cast<long double>(j) / c->pairs[a]) / kTwoPi;
-      h->tab.turns[at] = double(turns);
-      h->tab.fraction[at] = static_cast<uint64_t>(ldexpl(turns - floorl(turns), 64));
-      h->tab.axis[at] = static_cast<unsigned char>(a);
+      const double rounded = double(turns);
+      h->tab[0].turns[at] = static_cast<uint64_t>(ldexpl(turns - floorl(turns), 64));
+      std::memcpy(&h->tab[1].turns[at], &rounded, sizeof(rounded));
+      h->tab[0].axis[at] = h->tab[1].axis[at] = static_cast<unsigned char>(a);
     }
   *out = h;
   return TTT_OK;
@@ -276,16 +277,16 @@ extern "C" int ttt_rope_apply(const ttt_rope* h, int32_t B, int32_t H, int64_t N
   if (e == 2) {
     using T = __nv_bfloat16;
     if (one)
-      return wide == 16 ? launch_heads<T, 16, true>(a, h->tab, copy, st)
-             : wide == 8 ? launch_heads<T, 8, true>(a, h->tab, copy, st)
-                         : launch_heads<T, 4, true>(a, h->tab, copy, st);
-    return wide == 16 ? launch_heads<T, 16, false>(a, h->tab, copy, st)
-           : wide == 8 ? launch_heads<T, 8, false>(a, h->tab, copy, st)
-           : wide == 4 ? launch_heads<T, 4, false>(a, h->tab, copy, st)
-                       : launch_heads<T, 2, false>(a, h->tab, copy, st);
+      return wide == 16 ? launch_heads<T, 16, true>(a, h->tab[a.pos_f32], copy, st)
+             : wide == 8 ? launch_heads<T, 8, true>(a, h->tab[a.pos_f32], copy, st)
+                         : launch_heads<T, 4, true>(a, h->tab[a.pos_f32], copy, st);
+    return wide == 16 ? launch_heads<T, 16, false>(a, h->tab[a.pos_f32], copy, st)
+           : wide == 8 ? launch_heads<T, 8, false>(a, h->tab[a.pos_f32], copy, st)
+           : wide == 4 ? launch_heads<T, 4, false>(a, h->tab[a.pos_f32], copy, st)
+                       : launch_heads<T, 2, false>(a, h->tab[a.pos_f32], copy, st);
   }
-  if (one) return wide == 16 ? launch_heads<float, 16, true>(a, h->tab, copy, st) : launch_heads<float, 8, true>(a, h->tab, copy, st);
-  return wide == 16 ? launch_heads<float, 16, false>(a, h->tab, copy, st)
-         : wide == 8 ? launch_heads<float, 8, false>(a, h->tab, copy, st)
-                     : launch_heads<float, 4, false>(a, h->tab, copy, st);
+  if (one) return wide == 16 ? launch_heads<float, 16, true>(a, h->tab[a.pos_f32], copy, st) : launch_heads<float, 8, true>(a, h->tab[a.pos_f32], copy, st);
+  return wide == 16 ? launch_heads<float, 16, false>(a, h->tab[a.pos_f32], copy, st)
+         : wide == 8 ? launch_heads<float, 8, false>(a, h->tab[a.pos_f32], copy, st)
+                     : launch_heads<float, 4, false>(a, h->tab[a.pos_f32], copy, st);
 }

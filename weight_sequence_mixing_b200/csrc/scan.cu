@@ -772,11 +772,14 @@ __global__ void __launch_bounds__(128) scan_short_kernel(const __grid_constant__
 
 // Zeroes the rows behind the sequences' ends: a warp a row, the rows of a block one after the other
 template <class T>
-__global__ void __launch_bounds__(256) scan_clear_kernel(const int* lengths, T* y, int64_t sb, int64_t st, int64_t L, int D) {
-  const int b = blockIdx.y, lane = threadIdx.x % 32;
-  const int n = lengths[b];
-  for (int64_t t = max(n, 0) + int64_t(blockIdx.x) * 8 + threadIdx.x / 32; t < L; t += int64_t(gridDim.x) * 8)
-    for (int c = lane; c < D; c += 32) y[b * sb + t * st + c] = T(0.f);
+__global__ void __launch_bounds__(256) scan_clear_kernel(const int* lengths, T* y, int64_t sb, int64_t st, int64_t L, int B, int D) {
+  const int per = gridDim.x / B, lane = threadIdx.x % 32;  // blocks of a sequence; fewer than one: sequences of a block
+  for (int b = per ? blockIdx.x / per : blockIdx.x; b < B; b += per ? B : gridDim.x) {
+    const int first = per ? blockIdx.x % per : 0, hop = per ? per : 1;
+    if (first >= hop) break;
+    for (int64_t t = max(lengths[b], 0) + int64_t(first) * 8 + threadIdx.x / 32; t < L; t += int64_t(hop) * 8)
+      for (int c = lane; c < D; c += 32) y[b * sb + t * st + c] = T(0.f);
+  }
 }
 
 // Bytes of a call's workspace: the counter, then every tile's map and state.
@@ -1013,15 +1016,16 @@ extern "C" int ttt_scan_backward(const ttt_scan* h, int32_t B, int64_t L, const 
 extern "C" int ttt_scan_clear(const ttt_scan* h, int32_t B, int64_t L, const int32_t* lengths, void* y,
                               const ttt_strides* ys, void* stream) {
   if (!scan_sizes_ok(h, B, L) || !ys || !lengths || !is_aligned(lengths, 4)) return TTT_ERR_INVALID_ARG;
-  if (L > kMaxTokens || B > 65535) return TTT_ERR_UNSUPPORTED;
+  if (L > kMaxTokens) return TTT_ERR_UNSUPPORTED;
   const RowTensor in[] = {bytes(lengths, size_t(B) * 4)}, out[] = {rows(h, B, L, y, ys)};
   if (!apart(in, 1, out, 1)) return TTT_ERR_INVALID_ARG;
   if (L == 0) return TTT_OK;
-  const dim3 grid(unsigned(std::min<int64_t>(up(L, 8), std::max<int64_t>(1, 8 * 148 / B))), unsigned(B));
+  constexpr int64_t kBlocks = 8 * 148;
+  const unsigned grid = unsigned(B >= kBlocks ? kBlocks : B * std::min(up(L, 8), std::max<int64_t>(1, kBlocks / B)));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (h->cfg.dtype == TTT_BF16)
-    scan_clear_kernel<<<grid, 256, 0, st>>>(lengths, static_cast<__nv_bfloat16*>(y), ys->batch, ys->token, L, h->cfg.D);
+    scan_clear_kernel<<<grid, 256, 0, st>>>(lengths, static_cast<__nv_bfloat16*>(y), ys->batch, ys->token, L, B, h->cfg.D);
   else
-    scan_clear_kernel<<<grid, 256, 0, st>>>(lengths, static_cast<float*>(y), ys->batch, ys->token, L, h->cfg.D);
+    scan_clear_kernel<<<grid, 256, 0, st>>>(lengths, static_cast<float*>(y), ys->batch, ys->token, L, B, h->cfg.D);
   return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
 }
