@@ -26,6 +26,7 @@ namespace ttt {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kSmallThreads = 512;  // of a block that has a group to itself
 constexpr int kRun = 32;  // tokens summed about one value; a multiple of the loads under way
 
 struct NormArgs {
@@ -225,19 +226,29 @@ __global__ void __launch_bounds__(kThreads, 3) norm_parts_kernel(const __grid_co
   }
 }
 
-// The statistics of a group from its blocks' parts, by one warp
-__device__ __forceinline__ float2 join_parts(const NormArgs& p, int b, int g, int V) {
+// The blocks' parts of group g, by one warp: f(part, number of values) for each of the
+// lane's, in order, eight loads at a time.
+template <class F>
+__device__ __forceinline__ void for_parts(const NormArgs& p, int b, int g, int V, F&& f) {
   const int width = p.lanes * V, lane = threadIdx.x % 32;
   const int first = g * p.n / width, blocks = ((g + 1) * p.n - 1) / width - first + 1;
-  Part v = {0.f, 0.f, 0.f};
-  for (int e = lane; e < p.row_blocks * blocks; e += 32) {
-    const int rb = e / blocks, cb = first + e % blocks;
-    const int c0 = cb * width, c1 = min(p.C, c0 + width);
-    const float n = float(min(int64_t(p.range), p.N - int64_t(rb) * p.range)) * float(min((g + 1) * p.n, c1) - max(g * p.n, c0));
-    const float2 m = p.parts[((int64_t(b) * p.row_blocks + rb) * p.col_blocks + cb) * p.slots + g - c0 / p.n];
-    v = join(v, {n, m.x, m.y});
+  const int all = p.row_blocks * blocks;
+  for (int e0 = lane; e0 < all; e0 += 8 * 32) {
+    float2 m[8];
+    float n[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int e = e0 + 32 * k;
+      if (e >= all) break;
+      const int rb = blocks == 1 ? e : e / blocks, cb = first + e - rb * blocks;
+      const int c0 = cb * width, c1 = min(p.C, c0 + width);
+      m[k] = p.parts[((int64_t(b) * p.row_blocks + rb) * p.col_blocks + cb) * p.slots + g - c0 / p.n];
+      n[k] = float(min(int64_t(p.range), p.N - int64_t(rb) * p.range)) * float(min((g + 1) * p.n, c1) - max(g * p.n, c0));
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (e0 + 32 * k < all) f(m[k], n[k]);
   }
-  return finish(join_warp(v), p.eps);
 }
 
 // Joins the parts of its groups and normalises one range of tokens and block of channels.
@@ -254,7 +265,9 @@ __global__ void __launch_bounds__(kThreads, 3) norm_apply_kernel(const __grid_co
   const int c0 = cb * p.lanes * V, c1 = block_end(p, cb, V), g0 = c0 / p.n;
   cudaGridDependencySynchronize();  // the parts are there
   for (int g = g0 + threadIdx.x / 32; g <= (c1 - 1) / p.n; g += kThreads / 32) {
-    const float2 m = join_parts(p, b, g, V);
+    Part v = {0.f, 0.f, 0.f};
+    for_parts(p, b, g, V, [&](float2 m, float n) { v = join(v, {n, m.x, m.y}); });
+    const float2 m = finish(join_warp(v), p.eps);
     if (threadIdx.x % 32 == 0) {
       known[g - g0] = m;
       if (p.stats && rb == 0 && g * p.n >= c0)
@@ -470,14 +483,8 @@ __global__ void __launch_bounds__(kThreads, 2) norm_dx_kernel(const __grid_const
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();  // the sums are there
   for (int g = g0 + threadIdx.x / 32; g <= (c1 - 1) / p.n; g += kThreads / 32) {
-    const int width = p.lanes * V, first = g * p.n / width, blocks = ((g + 1) * p.n - 1) / width - first + 1;
     float q0 = 0.f, q1 = 0.f;
-    for (int e = threadIdx.x % 32; e < p.row_blocks * blocks; e += 32) {
-      const int64_t at = (int64_t(b) * p.row_blocks + e / blocks) * p.col_blocks + first + e % blocks;
-      const float2 s = p.parts[at * p.slots + g - (first + e % blocks) * width / p.n];
-      q0 += s.x;
-      q1 += s.y;
-    }
+    for_parts(p, b, g, V, [&](float2 s, float) { q0 += s.x, q1 += s.y; });
 #pragma unroll
     for (int m = 16; m; m /= 2) q0 += __shfl_xor_sync(~0u, q0, m), q1 += __shfl_xor_sync(~0u, q1, m);
     if (threadIdx.x % 32 == 0) known[g - g0] = make_float2(q0 * inv, q1 * inv);
@@ -551,55 +558,58 @@ __device__ __forceinline__ float2 block_sum(float2 v, float2* part) {
   __syncthreads();
   v = part[0];
 #pragma unroll
-  for (int i = 1; i < kThreads / 32; ++i) v.x += part[i].x, v.y += part[i].y;
+  for (int i = 1; i < kSmallThreads / 32; ++i) v.x += part[i].x, v.y += part[i].y;
   return v;
 }
 
 // lanes and rows: of the group's own channels
 template <class T, int BYTES, int ACT>
-__global__ void __launch_bounds__(kThreads) norm_small_kernel(const __grid_constant__ NormArgs p) {
+__global__ void __launch_bounds__(kSmallThreads) norm_small_kernel(const __grid_constant__ NormArgs p) {
   using X = Vec<T, BYTES>;
-  constexpr int V = X::N;
+  constexpr int V = X::N, kAtOnce = 8;
   extern __shared__ float values[];
-  __shared__ float2 part[kThreads / 32];
+  __shared__ float2 part[kSmallThreads / 32];
   const int g = blockIdx.x, b = blockIdx.y;
   const int row = threadIdx.x / p.lanes, lane = threadIdx.x % p.lanes;
-  const bool here = row < p.rows;
+  const int N = row < p.rows ? int(p.N) : 0;
   const T* x = static_cast<const T*>(p.x) + b * p.xs[0] + g * p.xs[1];
   T* y = static_cast<T*>(p.y) + b * p.ys[0] + g * p.ys[1];
-  const int N = int(p.N);
-  const float count = float(N) * float(p.n);
+  const float count = float(p.N) * float(p.n);
   float2 s = make_float2(0.f, 0.f);
-  if (here)
-    for (int t = row; t < N; t += p.rows)
-      for (int i = lane * V; i < p.n; i += p.lanes * V) {
-        X v;
-        v.load(x + t * p.xs[2] + i);
-        float f[V];
-        v.open(f);
+  for (int i = lane * V; i < p.n; i += p.lanes * V)
+    for (int t = row; t < N; t += kAtOnce * p.rows) {
+      X v[kAtOnce];
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          values[t * p.n + i + e] = f[e];
-          s.x += f[e];
+      for (int k = 0; k < kAtOnce; ++k)
+        if (t + k * p.rows < N) v[k].load(x + (t + k * p.rows) * p.xs[2] + i);
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+        if (t + k * p.rows < N) {
+          float f[V];
+          v[k].open(f);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            values[(t + k * p.rows) * p.n + i + e] = f[e];
+            s.x += f[e];
+          }
         }
-      }
+    }
   const float mean = block_sum(s, part).x / count;
   s = make_float2(0.f, 0.f);
-  if (here)
+  for (int i = lane * V; i < p.n; i += p.lanes * V)
+#pragma unroll 4
     for (int t = row; t < N; t += p.rows)
-      for (int i = lane * V; i < p.n; i += p.lanes * V)
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float d = values[t * p.n + i + e] - mean;
-          s.x = fmaf(d, d, s.x);
-          s.y += d;
-        }
+      for (int e = 0; e < V; ++e) {
+        const float d = values[t * p.n + i + e] - mean;
+        s.x = fmaf(d, d, s.x);
+        s.y += d;
+      }
   s = block_sum(s, part);
   // what the mean's rounding left over, taken off the variance and added to the mean
   const float off = s.y / count, centre = mean + off;
   const float rstd = 1.f / sqrtf(fmaxf(s.x / count - off * off, 0.f) + p.eps);
   if (p.stats && threadIdx.x == 0) reinterpret_cast<float2*>(p.stats)[int64_t(b) * p.G + g] = make_float2(centre, rstd);
-  if (!here) return;
   for (int i = lane * V; i < p.n; i += p.lanes * V) {
     float scale[V], shift[V];
 #pragma unroll
@@ -607,6 +617,7 @@ __global__ void __launch_bounds__(kThreads) norm_small_kernel(const __grid_const
       scale[e] = rstd * (p.weight ? p.weight[g * p.n + i + e] : 1.f);
       shift[e] = p.bias ? p.bias[g * p.n + i + e] : 0.f;
     }
+#pragma unroll 4
     for (int t = row; t < N; t += p.rows) {
       float f[V];
 #pragma unroll
@@ -621,20 +632,20 @@ __global__ void __launch_bounds__(kThreads) norm_small_kernel(const __grid_const
 
 // Backward of the same: xhat and dz in shared memory; a channel's sums by threads of its own
 template <class T, int BYTES, int ACT>
-__global__ void __launch_bounds__(kThreads) norm_small_grad_kernel(const __grid_constant__ NormArgs p) {
+__global__ void __launch_bounds__(kSmallThreads) norm_small_grad_kernel(const __grid_constant__ NormArgs p) {
   using X = Vec<T, BYTES>;
-  constexpr int V = X::N;
+  constexpr int V = X::N, kAtOnce = 4;
   extern __shared__ float values[];  // xhat, dz [N][n]; then [row][n] sums
-  __shared__ float2 part[kThreads / 32];
+  __shared__ float2 part[kSmallThreads / 32];
   const int g = blockIdx.x, b = blockIdx.y;
   const int row = threadIdx.x / p.lanes, lane = threadIdx.x % p.lanes;
   const bool here = row < p.rows;
+  const int N = here ? int(p.N) : 0;
   const T* x = static_cast<const T*>(p.x) + b * p.xs[0] + g * p.xs[1];
   const T* dy = static_cast<const T*>(p.dy) + b * p.dys[0] + g * p.dys[1];
   T* dx = static_cast<T*>(p.dx) + b * p.dxs[0] + g * p.dxs[1];
-  const int N = int(p.N);
-  float* const dzs = values + N * p.n;
-  float2* const sums = reinterpret_cast<float2*>(dzs + N * p.n);
+  float* const dzs = values + int(p.N) * p.n;
+  float2* const sums = reinterpret_cast<float2*>(dzs + int(p.N) * p.n);
   const float2 m = reinterpret_cast<const float2*>(p.stats)[int64_t(b) * p.G + g];
   float2 q = make_float2(0.f, 0.f);
   if (here)
@@ -645,22 +656,30 @@ __global__ void __launch_bounds__(kThreads) norm_small_grad_kernel(const __grid_
         w[e] = p.weight ? p.weight[g * p.n + i + e] : 1.f;
         o[e] = p.bias ? p.bias[g * p.n + i + e] : 0.f;
       }
-      for (int t = row; t < N; t += p.rows) {
-        X v, d;
-        v.load(x + t * p.xs[2] + i);
-        d.load(dy + t * p.dys[2] + i);
-        float f[V], h[V];
-        v.open(f);
-        d.open(h);
+      for (int t = row; t < N; t += kAtOnce * p.rows) {
+        X v[kAtOnce], d[kAtOnce];
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float xhat = (f[e] - m.x) * m.y;
-          const float dz = act_grad<T, ACT>(One{fmaf(xhat, w[e], o[e])}, One{h[e]}).v;
-          values[t * p.n + i + e] = xhat;
-          dzs[t * p.n + i + e] = dz;
-          s0[e] += dz;
-          s1[e] = fmaf(dz, xhat, s1[e]);
-        }
+        for (int k = 0; k < kAtOnce; ++k)
+          if (t + k * p.rows < N) {
+            v[k].load(x + (t + k * p.rows) * p.xs[2] + i);
+            d[k].load(dy + (t + k * p.rows) * p.dys[2] + i);
+          }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+          if (t + k * p.rows < N) {
+            float f[V], h[V];
+            v[k].open(f);
+            d[k].open(h);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              const float xhat = (f[e] - m.x) * m.y;
+              const float dz = act_grad<T, ACT>(One{fmaf(xhat, w[e], o[e])}, One{h[e]}).v;
+              values[(t + k * p.rows) * p.n + i + e] = xhat;
+              dzs[(t + k * p.rows) * p.n + i + e] = dz;
+              s0[e] += dz;
+              s1[e] = fmaf(dz, xhat, s1[e]);
+            }
+          }
       }
 #pragma unroll
       for (int e = 0; e < V; ++e) {
@@ -670,27 +689,27 @@ __global__ void __launch_bounds__(kThreads) norm_small_grad_kernel(const __grid_
       }
     }
   q = block_sum(q, part);
-  for (int c = threadIdx.x; c < p.n; c += kThreads) {
+  for (int c = threadIdx.x; c < p.n; c += kSmallThreads) {
     float2 s = sums[c];
     for (int r = 1; r < p.rows; ++r) s.x += sums[r * p.n + c].x, s.y += sums[r * p.n + c].y;
     p.channel_sums[int64_t(b) * p.C + g * p.n + c] = s;
   }
-  const float count = float(N) * float(p.n), m0 = q.x / count, m1 = q.y / count;
-  if (here)
-    for (int i = lane * V; i < p.n; i += p.lanes * V) {
-      float w[V];
+  const float count = float(p.N) * float(p.n), m0 = q.x / count, m1 = q.y / count;
+  for (int i = lane * V; i < p.n; i += p.lanes * V) {
+    float w[V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) w[e] = p.weight ? p.weight[g * p.n + i + e] : 1.f;
-      for (int t = row; t < N; t += p.rows) {
-        float f[V];
+    for (int e = 0; e < V; ++e) w[e] = p.weight ? p.weight[g * p.n + i + e] : 1.f;
+#pragma unroll 4
+    for (int t = row; t < N; t += p.rows) {
+      float f[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e)
-          f[e] = m.y * (dzs[t * p.n + i + e] * w[e] - m0 - values[t * p.n + i + e] * m1);
-        X v;
-        v.close(f);
-        v.store(dx + t * p.dxs[2] + i);
-      }
+      for (int e = 0; e < V; ++e)
+        f[e] = m.y * (dzs[t * p.n + i + e] * w[e] - m0 - values[t * p.n + i + e] * m1);
+      X v;
+      v.close(f);
+      v.store(dx + t * p.dxs[2] + i);
     }
+  }
 }
 
 // How a call is cut up: by the sizes and the number of bytes that its vectors take.
@@ -699,17 +718,18 @@ struct Cut {
   int lanes, rows, col_blocks, row_blocks, slots, smem;
   int32_t range;
 };
-constexpr int kSmallBytes = 96 * 1024;        // of a group in shared memory, as fp32
+constexpr int kSmallBytes = 96 * 1024;        // of shared memory that a group may take
+constexpr int kSmallValues = 16 * 1024;       // of a group, above which one block takes longer than two kernels
 constexpr int64_t kSmallTotal = 1 << 21;      // values in all, above which SMs are full either way
-// of 256 threads over a row's vectors
-void share(Cut& k, int vectors) {
-  k.lanes = std::min(vectors, kThreads);
-  k.rows = std::max(1, kThreads / k.lanes);
+// a block's threads over a row's vectors
+void share(Cut& k, int vectors, int threads) {
+  k.lanes = std::min(vectors, threads);
+  k.rows = std::max(1, threads / k.lanes);
 }
 // one block a group; V divides the group's channels
 Cut cut_small(int64_t N, int n, int V, bool backward) {
   Cut k{};
-  share(k, n / V);
+  share(k, n / V, kSmallThreads);
   k.rows = int(std::min<int64_t>(k.rows, N));
   k.small = true;
   k.smem = int(N * n * (backward ? 8 : 4) + (backward ? int64_t(k.rows) * n * 8 : 0));
@@ -717,15 +737,15 @@ Cut cut_small(int64_t N, int n, int V, bool backward) {
   return k;
 }
 bool fits_small(int32_t B, int64_t N, int C, int n, bool backward) {
-  // with a row of sums a thread at most, 2 kThreads floats a channel vector of one
-  const int64_t bytes = N * n * (backward ? 8 : 4) + (backward ? int64_t(std::max(n, kThreads)) * 8 * 8 : 0);
-  return B * N * C <= kSmallTotal && bytes <= kSmallBytes;
+  // the sums of the backward pass: rows of n channels, rows * n at most a thread's vector of 8 each (or one row)
+  const int64_t bytes = N * n * (backward ? 8 : 4) + (backward ? int64_t(std::max(n, 8 * kSmallThreads)) * 8 : 0);
+  return B * N * C <= kSmallTotal && N * n <= kSmallValues && bytes <= kSmallBytes;
 }
 Cut cut_blocks(int32_t B, int64_t N, int C, int G, int V, bool backward) {
   Cut k{};
   const int vectors = C / V;
   k.col_blocks = (vectors + kThreads - 1) / kThreads;
-  share(k, (vectors + k.col_blocks - 1) / k.col_blocks);
+  share(k, (vectors + k.col_blocks - 1) / k.col_blocks, kThreads);
   k.slots = std::min(G, k.lanes * V / (C / G) + 2);
   // as many blocks as run at once (three an SM forward, two backward), of 8 tokens a thread or more
   const int64_t most = std::max<int64_t>(1, (backward ? 2 : 3) * 148 / (int64_t(B) * k.col_blocks));
@@ -774,7 +794,7 @@ int launch_small(bool backward, NormArgs& a, const Cut& k, cudaStream_t st) {
   static OncePerDevice once[2];
   const auto f = backward ? norm_small_grad_kernel<T, BYTES, ACT> : norm_small_kernel<T, BYTES, ACT>;
   if (!allow_smem(f, once[backward])) return TTT_ERR_CUDA;
-  f<<<dim3(a.G, a.B), kThreads, k.smem, st>>>(a);
+  f<<<dim3(a.G, a.B), kSmallThreads, k.smem, st>>>(a);
   if (backward && (a.dweight || a.dbias)) launch_behind(norm_dweight_kernel, dim3((a.C + 31) / 32), 1024, 0, a, st);
   return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
 }

@@ -15,7 +15,7 @@
 //     of 16 bytes, by 4-byte asynchronous copies or plain loads).  Eight sweep a tile's
 //     rows twice: first for the maps, and one tile later, when the states that enter are
 //     there, for the states themselves.  Two follow the chain of states from tile to tile, the block's tiles in turn.
-//     So a tile's state is waited for while the next tile's maps are formed, and loads run
+//     (Without TMA the sweeping warps fetch their own rows.)  So a tile's state is waited for while the next tile's maps are formed, and loads run
 //     on throughout.  The gates are formed in both sweeps: keeping them (8 bytes a value
 //     in registers) was measured, and it holds too few tokens in flight for the chain's
 //     latency (scene layer of 1029120 tokens, 1024 channels: 5.98 ms, against 1.74 here).
@@ -47,9 +47,8 @@ namespace {
 
 constexpr int kWarps = 16;             // warps that sweep a tile's rows
 constexpr int kChainWarp = kWarps;     // two warps that follow the chain of states, tile about
-constexpr int kFeedWarp = kWarps + 2;  // the warp that fetches rows; without TMA the first of four
-constexpr int kFeeders = 4;
-constexpr int threads_of(bool tma) { return 32 * (kFeedWarp + (tma ? 1 : kFeeders)); }
+constexpr int kFeedWarp = kWarps + 2;  // the warp that hands out tiles and fetches their rows
+constexpr int kThreads = 32 * (kWarps + 3);
 constexpr int kRowBytes = 128;     // a tile's channels: 32 lanes of 4 bytes
 constexpr int kSave = 64;          // tokens from one kept state to the next
 constexpr int kShort = 16;         // longest sequence of the short form
@@ -321,8 +320,7 @@ struct Shape {
     float A[2][kWarps][32 * N];   // each warp's map: A,
     float H[2][kWarps][32 * N];   // and H, then in its place the state that enters the warp's rows
     float R[BACKWARD ? 2 : 1][BACKWARD ? kWarps : 1][32 * N];  // backward: the map A mu + R, then the mu that enters
-    uint64_t full[kStages], empty[kStages];  // a stage's rows are there; are done with
-    uint64_t posted[kStages];                // a stage's tile is known to the feeders
+    uint64_t full[kStages], empty[kStages];  // a stage's tile is known, and by TMA its rows are there; are done with
     uint64_t mapped[2], entered[2];          // a tile's maps are there; its states
     Job job[kStages];                        // the stages' tiles
     int abort;
@@ -330,8 +328,8 @@ struct Shape {
   static constexpr int kSmem = 1024 + kStages * kStageBytes + int(sizeof(Scratch));
 };
 
-// A feeder's share of one tensor's rows of a tile, from token t0 on, into shared memory at the
-// swizzle TMA uses.  Nothing is read where the size is 0: the word is filled with zero.
+// A warp's rows of one tensor's tile, from token t0 on, into shared memory at the swizzle TMA
+// uses.  Nothing is read where the size is 0: the word is filled with zero.
 template <class T, int ROWS>
 __device__ __forceinline__ void fetch(const ScanArgs& p, const void* base, const int64_t (&s)[2], int b, int c, int64_t t0,
                                       int64_t len, uint8_t* dst) {
@@ -363,7 +361,7 @@ __device__ __forceinline__ void fetch(const ScanArgs& p, const void* base, const
 }
 
 template <class T, int GATE, int INPUT, bool BACKWARD, bool TMA>
-__global__ void __launch_bounds__(threads_of(TMA), 1)
+__global__ void __launch_bounds__(kThreads, 1)
     scan_tile_kernel(const __grid_constant__ ScanArgs p, const __grid_constant__ CUtensorMap mg,
                      const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap md) {
   using S = Shape<T, BACKWARD>;
@@ -378,8 +376,7 @@ __global__ void __launch_bounds__(threads_of(TMA), 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sc.full[s], TMA ? 1 : 32 * kFeeders);
-      mbar_init(&sc.posted[s], 1);
+      mbar_init(&sc.full[s], 1);
       mbar_init(&sc.empty[s], kWarps);
     }
     for (int s = 0; s < 2; ++s) {
@@ -398,33 +395,6 @@ __global__ void __launch_bounds__(threads_of(TMA), 1)
     return __all_sync(~0u, ok) != 0;
   };
 
-  // this feeder's share of the rows of a stage's tile, without TMA
-  auto feed = [&](int s, const Job& job) {
-    constexpr int kShare = kTile / kFeeders;
-    if (job.t >= 0) {
-      const int f = (warp - kFeedWarp) * kShare, c = (job.at.col * 32 + lane) * N;
-      const int64_t t0 = int64_t(job.at.i) * kTile + f;
-      uint8_t* const to = stages + s * S::kStageBytes + f * kRowBytes;
-      fetch<T, kShare>(p, p.g, p.gs, job.at.b, c, t0, job.len, to);
-      fetch<T, kShare>(p, p.x, p.xs, job.at.b, c, t0, job.len, to + S::kBox);
-      if (BACKWARD) fetch<T, kShare>(p, p.dh, p.dhs, job.at.b, c, t0, job.len, to + 2 * S::kBox);
-    }
-    if (p.load == kLoad4)  // arrives when this lane's copies have
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sc.full[s])) : "memory");
-    else
-      mbar_arrive(&sc.full[s]);
-  };
-  if (!TMA && warp > kFeedWarp) {  // the first feeder's helpers
-    for (int k = 0, ends = 0; ends < 2; ++k) {
-      const int s = k % kStages;
-      if (!wait(&sc.posted[s], k / kStages)) break;
-      const Job job = sc.job[s];
-      feed(s, job);
-      ends += job.t < 0;
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    return;
-  }
   if (warp == kFeedWarp) {
     auto hand_out = [&](int turn) {
       int t = 0;
@@ -463,22 +433,17 @@ __global__ void __launch_bounds__(threads_of(TMA), 1)
       const Job job{more ? t : -1, int(len), at};
       if (lane == 0) sc.job[s] = job;
       __syncwarp();
-      if constexpr (TMA) {
-        if (lane == 0) {
+      if (lane == 0) {
+        if (TMA && more) {
           uint8_t* const to = stages + s * S::kStageBytes;
           const int c0 = at.col * 32 * N;
-          if (more) {
-            mbar_arrive_expect_tx(&sc.full[s], S::kStageBytes);
-            tma_load_3d(to, &mg, &sc.full[s], c0, int(t0), at.b);
-            tma_load_3d(to + S::kBox, &mx, &sc.full[s], c0, int(t0), at.b);
-            if (BACKWARD) tma_load_3d(to + 2 * S::kBox, &md, &sc.full[s], c0, int(t0), at.b);
-          } else {
-            mbar_arrive(&sc.full[s]);
-          }
+          mbar_arrive_expect_tx(&sc.full[s], S::kStageBytes);
+          tma_load_3d(to, &mg, &sc.full[s], c0, int(t0), at.b);
+          tma_load_3d(to + S::kBox, &mx, &sc.full[s], c0, int(t0), at.b);
+          if (BACKWARD) tma_load_3d(to + 2 * S::kBox, &md, &sc.full[s], c0, int(t0), at.b);
+        } else {
+          mbar_arrive(&sc.full[s]);
         }
-      } else {
-        if (lane == 0) mbar_arrive(&sc.posted[s]);
-        feed(s, job);
       }
       ++k;
     }
@@ -486,7 +451,6 @@ __global__ void __launch_bounds__(threads_of(TMA), 1)
     if (*(volatile int*)&sc.abort) {
       int given_up = 0;
       for (int m = k > kStages ? k - kStages : 0; m < k; ++m) mbar_wait(&sc.full[m % kStages], m / kStages & 1, &given_up);
-      asm volatile("cp.async.wait_all;" ::: "memory");
     }
     return;
   }
@@ -582,6 +546,35 @@ __global__ void __launch_bounds__(threads_of(TMA), 1)
   int swizzle[8];
 #pragma unroll
   for (int r = 0; r < 8; ++r) swizzle[r] = warp * kRows * kRowBytes + ((lane * 4) ^ (r << 4));
+  // Without TMA a warp fetches its own rows, kStages - 1 tiles ahead (the places of the tile
+  // that it has just done with); false if the wait for the tile ran out.
+  int fetched = 0;
+  bool more = true;
+  auto fetch_own = [&] {
+    if (more) {
+      const int s = fetched % kStages;
+      if (!wait(&sc.full[s], fetched / kStages)) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        return false;
+      }
+      const Job job = sc.job[s];
+      more = job.t >= 0;
+      if (more) {
+        const int c = (job.at.col * 32 + lane) * N;
+        const int64_t t0 = int64_t(job.at.i) * kTile + warp * kRows;
+        uint8_t* const to = stages + s * S::kStageBytes + warp * kRows * kRowBytes;
+        fetch<T, kRows>(p, p.g, p.gs, job.at.b, c, t0, job.len, to);
+        fetch<T, kRows>(p, p.x, p.xs, job.at.b, c, t0, job.len, to + S::kBox);
+        if (BACKWARD) fetch<T, kRows>(p, p.dh, p.dhs, job.at.b, c, t0, job.len, to + 2 * S::kBox);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    ++fetched;
+    return true;
+  };
+  if (!TMA)
+    for (int s = 0; s < kStages - 2; ++s)
+      if (!fetch_own()) return;
   Job cur{};
   cur.t = -1;
   for (int k = -1;; ++k) {
@@ -589,7 +582,12 @@ __global__ void __launch_bounds__(threads_of(TMA), 1)
     next.t = -1;
     if (k < 0 || cur.t >= 0) {
       const int s = (k + 1) % kStages, par = (k + 1) & 1;
+      if (!TMA && !fetch_own()) return;  // tile k + kStages - 1
       if (!wait(&sc.full[s], (k + 1) / kStages)) return;
+      if (!TMA) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");  // tile k + 1 is there
+        __syncwarp();
+      }
       next = sc.job[s];
       if (next.t >= 0) {
         const int left = next.len - (next.at.i * kTile + warp * kRows);
@@ -822,7 +820,7 @@ int launch(ScanArgs& a, const int64_t (*strides)[2], cudaStream_t st) {
   // all ones: nothing published, and a counter whose first answer is -1
   if (a.counter && cudaMemsetAsync(a.counter, 0xff, space_of(a.total, S::N).total, st) != cudaSuccess)
     return TTT_ERR_CUDA;
-  kernel<<<grid, threads_of(tma), S::kSmem, st>>>(a, m[0], m[1], m[2]);
+  kernel<<<grid, kThreads, S::kSmem, st>>>(a, m[0], m[1], m[2]);
   return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
 }
 

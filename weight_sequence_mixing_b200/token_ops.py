@@ -50,18 +50,22 @@ class NormConfig(ctypes.Structure):
                 ("dtype", ctypes.c_int32)]
 
 
-_STRIDES: dict = {}
+class _Strides(dict):
+    """ttt_strides by a tensor's strides (kept: a program has few, and a call needs several)."""
+
+    def __init__(self, convert):
+        super().__init__()
+        self._convert = convert
+
+    def __missing__(self, key):
+        if len(self) >= 4096:
+            self.clear()
+        s = self[key] = (ctypes.c_int64 * 3)(*self._convert(*key))
+        return s
 
 
-def _strides(batch: int, head: int, token: int):
-    """A ttt_strides of these values (kept: a program has few, and a call needs several)."""
-    key = (batch, head, token)
-    s = _STRIDES.get(key)
-    if s is None:
-        if len(_STRIDES) >= 4096:
-            _STRIDES.clear()
-        s = _STRIDES[key] = (ctypes.c_int64 * 3)(batch, head, token)
-    return s
+_HEADS = _Strides(lambda batch, head, token, _: (batch, head, token))
+_ROWS = _Strides(lambda batch, token, _: (batch, 0, token))
 
 
 def _ptr(t):
@@ -231,10 +235,9 @@ class RotaryPositions(_Op):
             out = _plain(x, shape, self.io_dtype)
         B, H, N, _ = shape
         if B and H and N:
-            xs, ys = x.stride(), out.stride()
-            st = LIB.ttt_rope_apply(handle, B, H, N, x.data_ptr(), _strides(xs[0], xs[1], xs[2]), pos.data_ptr(), kind,
-                                    N * self.axes if each else 0, out.data_ptr(), _strides(ys[0], ys[1], ys[2]),
-                                    inverse, _current_stream(self._index))
+            st = LIB.ttt_rope_apply(handle, B, H, N, x.data_ptr(), _HEADS[x.stride()], pos.data_ptr(), kind,
+                                    N * self.axes if each else 0, out.data_ptr(), _HEADS[out.stride()], inverse,
+                                    _current_stream(self._index))
             if st:
                 _check(st, "ttt_rope_apply")
         return out
@@ -286,9 +289,10 @@ class GatedScan(_StatusOp):
     def _new(self, handle, x, shape, lengths):
         out = _plain(x, shape, self.io_dtype)
         if lengths is not None:  # rows behind a sequence's end are left as they are: zeros, in a tensor made here
-            s = out.stride()
-            _check(LIB.ttt_scan_clear(handle, shape[0], shape[1], lengths.data_ptr(), out.data_ptr(),
-                                      _strides(s[0], 0, s[1]), _current_stream(self._index)), "ttt_scan_clear")
+            st = LIB.ttt_scan_clear(handle, shape[0], shape[1], lengths.data_ptr(), out.data_ptr(), _ROWS[out.stride()],
+                                    _current_stream(self._index))
+            if st:
+                _check(st, "ttt_scan_clear")
         return out
 
     def forward(self, g, x, h0=None, lengths=None, saved=None, out=None, h_last=None, stream=None):
@@ -316,11 +320,9 @@ class GatedScan(_StatusOp):
             h_last = _plain(x if h0 is None else h0, state, torch.float32)
         n = self._space[B, L]
         ws = self._bytes(n)
-        gs, xs, hs = g.stride(), x.stride(), out.stride()
-        st = LIB.ttt_scan_forward(handle, B, L, g.data_ptr(), _strides(gs[0], 0, gs[1]), x.data_ptr(),
-                                  _strides(xs[0], 0, xs[1]), _ptr(h0), _ptr(lengths), out.data_ptr(),
-                                  _strides(hs[0], 0, hs[1]), h_last.data_ptr(), _ptr(saved), _ptr(ws), n,
-                                  self._status_ptr, _current_stream(self._index))
+        st = LIB.ttt_scan_forward(handle, B, L, g.data_ptr(), _ROWS[g.stride()], x.data_ptr(), _ROWS[x.stride()], _ptr(h0),
+                                  _ptr(lengths), out.data_ptr(), _ROWS[out.stride()], h_last.data_ptr(), _ptr(saved),
+                                  _ptr(ws), n, self._status_ptr, _current_stream(self._index))
         if st:
             _check(st, "ttt_scan_forward")
         return out, h_last
@@ -347,10 +349,10 @@ class GatedScan(_StatusOp):
             dh0 = _plain(x if dh_last is None else dh_last, state, torch.float32)
         n = self._space[B, L]
         ws = self._bytes(n)
-        s = [_strides(t.stride(0), 0, t.stride(1)) for t in (dh, g, x, dg, dx)]
-        st = LIB.ttt_scan_backward(handle, B, L, dh.data_ptr(), s[0], _ptr(dh_last), g.data_ptr(), s[1], x.data_ptr(),
-                                   s[2], _ptr(lengths), saved.data_ptr(), dg.data_ptr(), s[3], dx.data_ptr(), s[4],
-                                   dh0.data_ptr(), _ptr(ws), n, self._status_ptr, _current_stream(self._index))
+        st = LIB.ttt_scan_backward(handle, B, L, dh.data_ptr(), _ROWS[dh.stride()], _ptr(dh_last), g.data_ptr(),
+                                   _ROWS[g.stride()], x.data_ptr(), _ROWS[x.stride()], _ptr(lengths), saved.data_ptr(),
+                                   dg.data_ptr(), _ROWS[dg.stride()], dx.data_ptr(), _ROWS[dx.stride()], dh0.data_ptr(),
+                                   _ptr(ws), n, self._status_ptr, _current_stream(self._index))
         if st:
             _check(st, "ttt_scan_backward")
         return dg, dx, dh0
@@ -370,13 +372,13 @@ class GroupNorm(_StatusOp):
         self._open(LIB.ttt_norm_create, LIB.ttt_norm_destroy, k)
         self.C, self.groups = int(c["C"]), int(c["groups"])
         self._space = _Sizes(lambda B, N, backward: LIB.ttt_norm_workspace_size(self._handle, B, N, backward))
-        self._each = self.C // self.groups  # channels of a group
+        each = self._each = self.C // self.groups  # channels of a group
+        self._channels_last = _Strides(lambda batch, token, _: (batch, each, token))
 
     def new_stats(self, B: int, stream=None):
         """A buffer for the mean and 1 / sqrt(var + eps) of every group, for the backward call."""
         self._open_handle()
-        return self._run(stream, (), lambda: torch.empty((B, self.groups, 2), dtype=torch.float32,
-                                                         device=self._status.device))
+        return self._run(stream, (), _plain, self._status.view(torch.float32), (B, self.groups, 2), torch.float32)
 
     def _shapes(self, x):
         """(shape x has to have, [B, N, C])"""
@@ -391,9 +393,9 @@ class GroupNorm(_StatusOp):
             raise ValueError(f"x: no statistics of an empty tensor, got shape {tuple(s)}")
         return want, rows
 
-    def _strides(self, t):
+    def _by_group(self, t):
         s = t.stride()
-        return _strides(s[0], self._each, s[1]) if len(s) == 3 else _strides(s[0], s[1], s[2])
+        return self._channels_last[s] if len(s) == 3 else _HEADS[s]
 
     def forward(self, x, weight=None, bias=None, stats=None, out=None, stream=None):
         """y [B, N, C].  weight, bias: [C] fp32.  out: given, and then possibly x itself, or new."""
@@ -415,8 +417,8 @@ class GroupNorm(_StatusOp):
             out = _plain(x, rows, self.io_dtype)
         n = self._space[rows[0], rows[1], 0]
         ws = self._bytes(n)
-        st = LIB.ttt_norm_forward(handle, rows[0], rows[1], x.data_ptr(), self._strides(x), _ptr(weight), _ptr(bias),
-                                  out.data_ptr(), self._strides(out), _ptr(stats), _ptr(ws), n, self._status_ptr,
+        st = LIB.ttt_norm_forward(handle, rows[0], rows[1], x.data_ptr(), self._by_group(x), _ptr(weight), _ptr(bias),
+                                  out.data_ptr(), self._channels_last[out.stride()], _ptr(stats), _ptr(ws), n, self._status_ptr,
                                   _current_stream(self._index))
         if st:
             _check(st, "ttt_norm_forward")
@@ -445,9 +447,9 @@ class GroupNorm(_StatusOp):
             dbias = _plain(x if bias is None else bias, (self.C,), torch.float32)
         n = self._space[rows[0], rows[1], 1]
         ws = self._bytes(n)
-        st = LIB.ttt_norm_backward(handle, rows[0], rows[1], dy.data_ptr(), self._strides(dy), x.data_ptr(),
-                                   self._strides(x), _ptr(weight), _ptr(bias), stats.data_ptr(), dx.data_ptr(),
-                                   self._strides(dx), dweight.data_ptr(), dbias.data_ptr(), _ptr(ws), n,
+        st = LIB.ttt_norm_backward(handle, rows[0], rows[1], dy.data_ptr(), self._channels_last[dy.stride()], x.data_ptr(),
+                                   self._by_group(x), _ptr(weight), _ptr(bias), stats.data_ptr(), dx.data_ptr(),
+                                   self._by_group(dx), dweight.data_ptr(), dbias.data_ptr(), _ptr(ws), n,
                                    self._status_ptr, _current_stream(self._index))
         if st:
             _check(st, "ttt_norm_backward")
