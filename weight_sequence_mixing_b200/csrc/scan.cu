@@ -316,13 +316,14 @@ struct Shape {
   static constexpr int kTensors = BACKWARD ? 3 : 2;
   static constexpr int kStages = BACKWARD ? 4 : 3;
   static constexpr int kStageBytes = kTensors * kBox;
+  static constexpr int kMostJobs = kStages + 2;
   struct Scratch {  // behind the stages; two of each by parity of the block's tiles
     float A[2][kWarps][32 * N];   // each warp's map: A,
     float H[2][kWarps][32 * N];   // and H, then in its place the state that enters the warp's rows
     float R[BACKWARD ? 2 : 1][BACKWARD ? kWarps : 1][32 * N];  // backward: the map A mu + R, then the mu that enters
-    uint64_t full[kStages], empty[kStages];  // a stage's tile is known, and by TMA its rows are there; are done with
+    uint64_t full[kMostJobs], empty[kMostJobs];  // a tile is known, and by TMA its rows are there; is done with
     uint64_t mapped[2], entered[2];          // a tile's maps are there; its states
-    Job job[kStages];                        // the stages' tiles
+    Job job[kMostJobs];
     int abort;
   };
   static constexpr int kSmem = 1024 + kStages * kStageBytes + int(sizeof(Scratch));
@@ -368,6 +369,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   using W = Word<T>;
   using V = typename W::V;
   constexpr int N = S::N, kStages = S::kStages, kTile = S::kTile, kRows = S::kRows;
+  // tiles handed to the block at a time; without TMA two more than stages, so that a warp whose own
+  // places are free need not wait for the others
+  constexpr int kJobs = TMA ? kStages : S::kMostJobs;
   extern __shared__ uint8_t raw[];
   uint8_t* const stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   typename S::Scratch& sc = *reinterpret_cast<typename S::Scratch*>(stages + kStages * S::kStageBytes);
@@ -375,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int step = p.B * p.cols;  // tiles from one of a column to its next
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kJobs; ++s) {
       mbar_init(&sc.full[s], 1);
       mbar_init(&sc.empty[s], kWarps);
     }
@@ -428,21 +432,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
       }
-      const int s = k % kStages;
-      if (k >= kStages && !wait(&sc.empty[s], k / kStages - 1)) break;
+      const int s = k % kStages, q = k % kJobs;
+      if (k >= kJobs && !wait(&sc.empty[q], k / kJobs - 1)) break;
       const Job job{more ? t : -1, int(len), at};
-      if (lane == 0) sc.job[s] = job;
+      if (lane == 0) sc.job[q] = job;
       __syncwarp();
       if (lane == 0) {
         if (TMA && more) {
           uint8_t* const to = stages + s * S::kStageBytes;
           const int c0 = at.col * 32 * N;
-          mbar_arrive_expect_tx(&sc.full[s], S::kStageBytes);
-          tma_load_3d(to, &mg, &sc.full[s], c0, int(t0), at.b);
-          tma_load_3d(to + S::kBox, &mx, &sc.full[s], c0, int(t0), at.b);
-          if (BACKWARD) tma_load_3d(to + 2 * S::kBox, &md, &sc.full[s], c0, int(t0), at.b);
+          mbar_arrive_expect_tx(&sc.full[q], S::kStageBytes);
+          tma_load_3d(to, &mg, &sc.full[q], c0, int(t0), at.b);
+          tma_load_3d(to + S::kBox, &mx, &sc.full[q], c0, int(t0), at.b);
+          if (BACKWARD) tma_load_3d(to + 2 * S::kBox, &md, &sc.full[q], c0, int(t0), at.b);
         } else {
-          mbar_arrive(&sc.full[s]);
+          mbar_arrive(&sc.full[q]);
         }
       }
       ++k;
@@ -450,16 +454,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     // copies in flight end before the block does: after a wait that ran out, nobody else waits for them
     if (*(volatile int*)&sc.abort) {
       int given_up = 0;
-      for (int m = k > kStages ? k - kStages : 0; m < k; ++m) mbar_wait(&sc.full[m % kStages], m / kStages & 1, &given_up);
+      for (int m = k > kJobs ? k - kJobs : 0; m < k; ++m) mbar_wait(&sc.full[m % kJobs], m / kJobs & 1, &given_up);
     }
     return;
   }
 
   if (warp >= kChainWarp) {
     for (int k = warp - kChainWarp;; k += 2) {
-      const int s = k % kStages, par = k & 1;
-      if (!wait(&sc.full[s], k / kStages)) return;
-      const Job job = sc.job[s];
+      const int par = k & 1;
+      if (!wait(&sc.full[k % kJobs], k / kJobs)) return;
+      const Job job = sc.job[k % kJobs];
       const int t = job.t;
       if (t < 0) return;
       const Place at = job.at;
@@ -553,11 +557,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto fetch_own = [&] {
     if (more) {
       const int s = fetched % kStages;
-      if (!wait(&sc.full[s], fetched / kStages)) {
+      if (!wait(&sc.full[fetched % kJobs], fetched / kJobs)) {
         asm volatile("cp.async.wait_all;" ::: "memory");
         return false;
       }
-      const Job job = sc.job[s];
+      const Job job = sc.job[fetched % kJobs];
       more = job.t >= 0;
       if (more) {
         const int c = (job.at.col * 32 + lane) * N;
@@ -583,12 +587,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (k < 0 || cur.t >= 0) {
       const int s = (k + 1) % kStages, par = (k + 1) & 1;
       if (!TMA && !fetch_own()) return;  // tile k + kStages - 1
-      if (!wait(&sc.full[s], (k + 1) / kStages)) return;
+      if (!wait(&sc.full[(k + 1) % kJobs], (k + 1) / kJobs)) return;
       if (!TMA) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");  // tile k + 1 is there
         __syncwarp();
       }
-      next = sc.job[s];
+      next = sc.job[(k + 1) % kJobs];
       if (next.t >= 0) {
         const int left = next.len - (next.at.i * kTile + warp * kRows);
         const uint8_t* const stage = stages + s * S::kStageBytes;
@@ -701,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sc.empty[s]);
+      if (lane == 0) mbar_arrive(&sc.empty[k % kJobs]);
     }
     cur = next;
   }
