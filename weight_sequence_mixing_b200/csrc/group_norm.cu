@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_apply_kernel(const __grid_co
   using X = Vec<T, BYTES>;
   using P = typename X::P;
   // a pack's mean is shared by the packs of kStep channels
-  constexpr int V = X::N, K = V / Q, kPacks = X::kPacks, kStep = Q > P::N ? Q : P::N, kMeans = V / kStep, kAtOnce = 8;
+  constexpr int V = X::N, K = V / Q, kPacks = X::kPacks, kStep = Q > P::N ? Q : P::N, kMeans = V / kStep, kAtOnce = 6;
   extern __shared__ float2 known[];  // (mean, 1 / std) of the block's groups
   const int cb = gridDim.x - 1 - blockIdx.x, rb = gridDim.y - 1 - blockIdx.y, b = gridDim.z - 1 - blockIdx.z;
   const Column k = column(p, cb, V);

@@ -51,12 +51,15 @@ struct RopeArgs {
 // output's 2^-9), fp32 sincospif.
 // Measured against this (196608 tokens x 2 heads x 512 bf16, 139 us; the copy of as many bytes 123): angles in fp64 and
 // one (token, heads) step ahead, 200 us; angles of a tile shared in shared memory, 211 us.
+// tokens of a thread: eight or four steps in all, of which a head takes one
+constexpr int tokens_of(int bytes, bool one, int heads) { return std::max(1, (one || bytes < 16 ? 8 : 4) / heads); }
+
 template <class T, int BYTES, bool ONE, int HEADS, bool POS_F32>
 __global__ void __launch_bounds__(256, ONE ? 3 : 2)
     rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopeTable tab) {
   using X = Vec<T, BYTES>;
   constexpr int P = ONE ? X::N / 2 : X::N;  // pairs of a thread
-  constexpr int kTokens = (ONE || BYTES < 16 ? 8 : 4) / HEADS;
+  constexpr int kTokens = tokens_of(BYTES, ONE, HEADS);
   const int item = blockIdx.x % a.item_blocks * a.lanes + threadIdx.x % a.lanes;
   const int row = threadIdx.x / a.lanes;
   if (row >= a.rows || item >= a.items) return;
@@ -165,7 +168,7 @@ __global__ void __launch_bounds__(256, ONE ? 3 : 2)
 template <class T, int BYTES, bool ONE, int HEADS>
 int launch(RopeArgs& a, const RopeTable& tab, bool copy, cudaStream_t st) {
   constexpr int V = BYTES / int(sizeof(T)), P = ONE ? V / 2 : V;
-  constexpr int kTokens = (ONE || BYTES < 16 ? 8 : 4) / HEADS;
+  constexpr int kTokens = tokens_of(BYTES, ONE, HEADS);
   a.units = a.pairs / P;
   a.items = a.units + (copy ? (a.d - 2 * a.pairs) / V : 0);
   a.item_blocks = (a.items + 255) / 256;
@@ -183,13 +186,16 @@ int launch(RopeArgs& a, const RopeTable& tab, bool copy, cudaStream_t st) {
 }
 
 // Heads of a thread: those that share its angles, the most that leave no more than one of
-// all heads' places empty.  Narrow vectors have one form.
+// all heads' places empty (48672 tokens x 6 heads x 64 in halves: 14.1 us with six heads a
+// thread, 15.7 with three, 16.0 with two).  Narrow vectors have one form.
 template <class T, int BYTES, bool ONE>
 int launch_heads(RopeArgs& a, const RopeTable& tab, bool copy, cudaStream_t st) {
   if constexpr (BYTES < 16) {
     return launch<T, BYTES, ONE, 2>(a, tab, copy, st);
   } else {
     if (a.H == 1) return launch<T, BYTES, ONE, 1>(a, tab, copy, st);
+    if constexpr (!ONE)
+      if (a.H % 6 == 0) return launch<T, BYTES, ONE, 6>(a, tab, copy, st);
     if (a.H % 4 == 0 || a.H % 4 == 3) return launch<T, BYTES, ONE, 4>(a, tab, copy, st);
     return launch<T, BYTES, ONE, 2>(a, tab, copy, st);
   }
