@@ -1,5 +1,6 @@
 """Build step of the CUDA library: compiles csrc/*.cu for sm_100a with nvcc and
-links them, with the static CUDA runtime, into libttt_b200.so next to this file.
+links them, with the static CUDA runtime, into libttt_b200.so next to this file; then
+the Python module _token_ops (csrc/token_ops_py.cpp), which calls it on torch tensors.
 
 Object files go to ../_build (ignored by git); a source whose text and flags are
 unchanged since the last build is not recompiled.
@@ -20,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libttt_b200.so")
+MODULE = os.path.join(PKG, "_token_ops.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
@@ -86,5 +88,34 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     return LIB
 
 
+def build_module(verbose: bool = False) -> str:
+    """Compile and link the Python module _token_ops against torch and libttt_b200.so; returns its path."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    src = os.path.join(CSRC, "token_ops_py.cpp")
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    includes = [sysconfig.get_paths()["include"], INCLUDE, os.path.join(cuda, "include")] + cpp_extension.include_paths()
+    flags = ["-std=c++17", "-O2", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    flags += [f for d in includes for f in ("-isystem", d)]
+    flags += [f"-L{d}" for d in cpp_extension.library_paths()]
+    libs = ["-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-L{PKG}", "-l:libttt_b200.so",
+            "-Wl,-rpath,$ORIGIN"]
+    built = os.path.join(BUILD, f"_token_ops.{_digest(src, flags + libs + [torch.__version__, sys.version])}.so")
+    if not os.path.exists(built):
+        cmd = ["g++"] + flags + ["-o", built + ".tmp", src] + libs
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        subprocess.run(cmd, check=True)
+        os.replace(built + ".tmp", built)
+    if not os.path.exists(MODULE) or open(MODULE, "rb").read() != open(built, "rb").read():
+        shutil.copyfile(built, MODULE + ".tmp")
+        os.replace(MODULE + ".tmp", MODULE)
+    return MODULE
+
+
 if __name__ == "__main__":
     print(build(verbose="-v" in sys.argv))
+    print(build_module(verbose="-v" in sys.argv))
