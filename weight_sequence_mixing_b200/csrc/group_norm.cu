@@ -16,6 +16,7 @@
 #include <algorithm>
 #include <new>
 
+#include "gelu_fwd.cuh"
 #include "op_checks.h"
 #include "per_device.h"
 #include "tc_gemm.cuh"
@@ -49,21 +50,40 @@ struct NormArgs {
 struct Part {  // of n values: their mean, and S the sum of squares about it
   float n, mean, S;
 };
-__device__ __forceinline__ Part join(const Part& a, const Part& b) {
-  const float n = a.n + b.n;
-  if (b.n == 0.f) return a;
-  if (a.n == 0.f) return b;
-  const float d = b.mean - a.mean, f = b.n / n;
-  return {n, fmaf(d, f, a.mean), a.S + b.S + d * d * a.n * f};
-}
-// over a warp, lane 0 first; every lane has the result
-__device__ __forceinline__ Part join_warp(Part v) {
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-  for (int m = 1; m < 32; m *= 2) {
-    const Part o = {__shfl_down_sync(~0u, v.n, m), __shfl_down_sync(~0u, v.mean, m), __shfl_down_sync(~0u, v.S, m)};
-    v = join(v, o);
-  }
-  return {__shfl_sync(~0u, v.n, 0), __shfl_sync(~0u, v.mean, 0), __shfl_sync(~0u, v.S, 0)};
+  for (int m = 16; m; m /= 2) v += __shfl_xor_sync(~0u, v, m);
+  return v;
+}
+// Joins `all` parts, the warp's lanes taking them in turn: first the mean (about the first
+// part's, so that it keeps its digits), then S about it.  get(e, part) loads part e; its n may
+// be 0 but for the first.  Up to 256 parts are loaded once, all loads before the first sum;
+// more are loaded again for the second.
+template <class F>
+__device__ __forceinline__ Part join_parts(int all, F&& get) {
+  constexpr int kHeld = 8;
+  const int lane = threadIdx.x % 32;
+  Part first, v[kHeld];
+  get(0, first);
+  auto pass = [&](auto&& add, bool again) {
+    for (int e0 = lane; e0 < all; e0 += kHeld * 32) {
+      if (again) {
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k)
+          if (e0 + 32 * k < all) get(e0 + 32 * k, v[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k)
+        if (e0 + 32 * k < all) add(v[k]);
+    }
+  };
+  float n = 0.f, s = 0.f;
+  pass([&](const Part& v) { n += v.n, s = fmaf(v.n, v.mean - first.mean, s); }, true);
+  n = warp_sum(n);
+  const float mean = first.mean + warp_sum(s) / n;
+  float S = 0.f;
+  pass([&](const Part& v) { S += fmaf(v.n * (v.mean - mean), v.mean - mean, v.S); }, all > kHeld * 32);
+  return {n, mean, warp_sum(S)};
 }
 __device__ __forceinline__ float2 finish(const Part& v, float eps) {  // mean, 1 / sqrt(var + eps)
   return make_float2(v.mean, 1.f / sqrtf(v.S / v.n + eps));
@@ -80,15 +100,31 @@ __device__ __forceinline__ P sigmoid(P z) {
     e = each(mul_(z, P::all(-1.4426950408889634f)), [](float v) { return exp2_fast(v); });
   return each(add_(e, P::all(1.f)), [](float v) { return rcp_fast(v); });
 }
+// z Phi(z) and its slope Phi(z) + z phi(z): bf16 outputs by the published approximations that
+// the layer's MLP uses (Phi 1.5e-7 off at most), fp32 ones by the library's erfc.
 constexpr float kInvSqrt2 = 0.70710678118654752f, kInvSqrt2Pi = 0.39894228040143268f;
-template <class P>
-__device__ __forceinline__ P normal_cdf(P z) {
-  return each(z, [](float v) { return 0.5f * erfcf(v * -kInvSqrt2); });
+template <class T>
+__device__ __forceinline__ One gelu(One z) {
+  if (sizeof(T) == 2) return {gelu_fwd2(make_float2(z.v, z.v)).x};
+  return {z.v * 0.5f * erfcf(z.v * -kInvSqrt2)};
+}
+template <class T>
+__device__ __forceinline__ Two gelu(Two z) {
+  if (sizeof(T) == 4) return two(gelu<T>(One{z[0]}).v, gelu<T>(One{z[1]}).v);
+  const float2 y = gelu_fwd2(make_float2(z[0], z[1]));
+  return two(y.x, y.y);
+}
+template <class T>
+__device__ __forceinline__ float gelu_slope(float z) {
+  if (sizeof(T) == 4) return fmaf(z * kInvSqrt2Pi, expf(-0.5f * z * z), 0.5f * erfcf(z * -kInvSqrt2));
+  float cdf, pdf;
+  normal_cdf_pdf(z, cdf, pdf);
+  return fmaf(z, pdf, cdf);
 }
 template <class T, int ACT, class P>
 __device__ __forceinline__ P act(P z) {
   if constexpr (ACT == TTT_ACT_SILU) return mul_(z, sigmoid<T>(z));
-  if constexpr (ACT == TTT_ACT_GELU) return mul_(z, normal_cdf(z));
+  if constexpr (ACT == TTT_ACT_GELU) return gelu<T>(z);
   return z;
 }
 // the activation's slope at z, times dy
@@ -98,10 +134,7 @@ __device__ __forceinline__ P act_grad(P z, P dy) {
     const P s = sigmoid<T>(z);
     return mul_(dy, fma_(mul_(z, s), sub_(P::all(1.f), s), s));
   }
-  if constexpr (ACT == TTT_ACT_GELU) {
-    const P d = each(z, [](float v) { return kInvSqrt2Pi * expf(-0.5f * v * v); });
-    return mul_(dy, fma_(z, d, normal_cdf(z)));
-  }
+  if constexpr (ACT == TTT_ACT_GELU) return mul_(dy, each(z, [](float v) { return gelu_slope<T>(v); }));
   return dy;
 }
 
@@ -210,46 +243,49 @@ __global__ void __launch_bounds__(kThreads, 3) norm_parts_kernel(const __grid_co
   }
   __syncthreads();
   const int c0 = cb * width, c1 = block_end(p, cb, V), g0 = c0 / p.n;
-  const int lane = threadIdx.x % 32;
+  const int lane = threadIdx.x % 32, each = tokens / p.rows, more = tokens - each * p.rows;  // tokens of a thread
   for (int g = g0 + threadIdx.x / 32; g <= (c1 - 1) / p.n; g += kThreads / 32) {
     const int from = (max(g * p.n, c0) - c0) / Q, wide = (min((g + 1) * p.n, c1) - c0) / Q - from;
-    Part v = {0.f, 0.f, 0.f};
-    for (int e = lane; e < p.rows * wide; e += 32) {
+    const Part v = join_parts(p.rows * wide, [&](int e, Part& v) {
       const int r = e / wide;
-      const float n = tokens > r ? float((tokens - r + p.rows - 1) / p.rows * Q) : 0.f;
-      const float2 m = threads[r * (p.lanes * K) + from + e % wide];
-      v = join(v, {n, m.x, m.y});
-    }
-    v = join_warp(v);
+      const float2 m = threads[r * (p.lanes * K) + from + e - r * wide];
+      v = {float((each + (r < more ? 1 : 0)) * Q), m.x, m.y};
+    });
     if (lane == 0)
       p.parts[((int64_t(b) * p.row_blocks + rb) * p.col_blocks + cb) * p.slots + g - g0] = make_float2(v.mean, v.S);
   }
 }
 
-// The blocks' parts of group g, by one warp: f(part, number of values) for each of the
-// lane's, in order, eight loads at a time.
-template <class F>
-__device__ __forceinline__ void for_parts(const NormArgs& p, int b, int g, int V, F&& f) {
-  const int width = p.lanes * V, lane = threadIdx.x % 32;
-  const int first = g * p.n / width, blocks = ((g + 1) * p.n - 1) / width - first + 1;
-  const int all = p.row_blocks * blocks;
-  for (int e0 = lane; e0 < all; e0 += 8 * 32) {
-    float2 m[8];
-    float n[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int e = e0 + 32 * k;
-      if (e >= all) break;
-      const int rb = blocks == 1 ? e : e / blocks, cb = first + e - rb * blocks;
-      const int c0 = cb * width, c1 = min(p.C, c0 + width);
-      m[k] = p.parts[((int64_t(b) * p.row_blocks + rb) * p.col_blocks + cb) * p.slots + g - c0 / p.n];
-      n[k] = float(min(int64_t(p.range), p.N - int64_t(rb) * p.range)) * float(min((g + 1) * p.n, c1) - max(g * p.n, c0));
+// Where the blocks' parts of group g are, and how many values each is of.  Where all lie in
+// one block of channels (the usual case) they are a row apart and of `each` values, the last
+// of `end`.
+struct PartsOf {
+  const NormArgs& p;
+  const float2* parts;
+  int g, width, first, blocks, all, hop;
+  float each, end;
+  __device__ __forceinline__ PartsOf(const NormArgs& p, int b, int g, int V) : p(p), g(g), width(p.lanes * V) {
+    first = g * p.n / width, blocks = ((g + 1) * p.n - 1) / width - first + 1;
+    all = p.row_blocks * blocks;
+    hop = p.col_blocks * p.slots;
+    each = float(p.range), end = float(p.N - int64_t(p.row_blocks - 1) * p.range);
+    parts = p.parts + int64_t(b) * p.row_blocks * hop;
+    if (blocks == 1) {
+      each *= float(p.n), end *= float(p.n);
+      parts += first * p.slots + g - first * width / p.n;
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (e0 + 32 * k < all) f(m[k], n[k]);
   }
-}
+  __device__ __forceinline__ float2 at(int e, float* values) const {
+    if (blocks == 1) {
+      *values = e == all - 1 ? end : each;
+      return parts[int64_t(e) * hop];
+    }
+    const int rb = e / blocks, cb = first + e - rb * blocks, c0 = cb * width;
+    const float n = float(min((g + 1) * p.n, min(p.C, c0 + width)) - max(g * p.n, c0));
+    *values = (rb == p.row_blocks - 1 ? end : each) * n;
+    return parts[int64_t(rb) * hop + cb * p.slots + g - c0 / p.n];
+  }
+};
 
 // Joins the parts of its groups and normalises one range of tokens and block of channels.
 template <class T, int BYTES, int Q, int ACT>
@@ -265,9 +301,13 @@ __global__ void __launch_bounds__(kThreads, 3) norm_apply_kernel(const __grid_co
   const int c0 = cb * p.lanes * V, c1 = block_end(p, cb, V), g0 = c0 / p.n;
   cudaGridDependencySynchronize();  // the parts are there
   for (int g = g0 + threadIdx.x / 32; g <= (c1 - 1) / p.n; g += kThreads / 32) {
-    Part v = {0.f, 0.f, 0.f};
-    for_parts(p, b, g, V, [&](float2 m, float n) { v = join(v, {n, m.x, m.y}); });
-    const float2 m = finish(join_warp(v), p.eps);
+    const PartsOf of(p, b, g, V);
+    const float2 m = finish(join_parts(of.all,
+                                       [&](int e, Part& v) {
+                                         const float2 m = of.at(e, &v.n);
+                                         v.mean = m.x, v.S = m.y;
+                                       }),
+                            p.eps);
     if (threadIdx.x % 32 == 0) {
       known[g - g0] = m;
       if (p.stats && rb == 0 && g * p.n >= c0)
@@ -484,7 +524,17 @@ __global__ void __launch_bounds__(kThreads, 2) norm_dx_kernel(const __grid_const
   cudaGridDependencySynchronize();  // the sums are there
   for (int g = g0 + threadIdx.x / 32; g <= (c1 - 1) / p.n; g += kThreads / 32) {
     float q0 = 0.f, q1 = 0.f;
-    for_parts(p, b, g, V, [&](float2 s, float) { q0 += s.x, q1 += s.y; });
+    const PartsOf of(p, b, g, V);
+    for (int e0 = threadIdx.x % 32; e0 < of.all; e0 += 8 * 32) {
+      float2 s[8];
+      float n;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (e0 + 32 * k < of.all) s[k] = of.at(e0 + 32 * k, &n);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (e0 + 32 * k < of.all) q0 += s[k].x, q1 += s[k].y;
+    }
 #pragma unroll
     for (int m = 16; m; m /= 2) q0 += __shfl_xor_sync(~0u, q0, m), q1 += __shfl_xor_sync(~0u, q1, m);
     if (threadIdx.x % 32 == 0) known[g - g0] = make_float2(q0 * inv, q1 * inv);
