@@ -168,10 +168,11 @@ __device__ __forceinline__ int64_t length_of(const ScanArgs& p, int b) {
 struct Place {
   int b, col, i;  // batch entry, column of channels, tile of the sequence in token order
 };
-struct Job {
+struct alignas(16) Job {
   int t;    // the tile's number as handed out, or -1: no more
   int len;  // tokens of its sequence
-  Place at;
+  int col, i, b;
+  int64_t out[2];  // the tile's first element in the outputs: h; or dx and dg
 };
 template <bool BACKWARD>
 __device__ __forceinline__ Place place_of(const ScanArgs& p, int t) {
@@ -305,8 +306,8 @@ __device__ __forceinline__ void put_word(const ScanArgs& p, T* to, int c, typena
   }
 }
 
-// Tiles of 128 tokens forward and 64 backward (one tensor more), three and four stages:
-// 96 KB, two blocks an SM.
+// Tiles of 256 tokens forward and 128 backward (one tensor more), three and four stages:
+// 192 KB, one block an SM.
 template <class T, bool BACKWARD>
 struct Shape {
   static constexpr int N = Word<T>::N;
@@ -318,9 +319,10 @@ struct Shape {
   static constexpr int kStageBytes = kTensors * kBox;
   static constexpr int kMostJobs = kStages + 2;
   struct Scratch {  // behind the stages; two of each by parity of the block's tiles
-    float A[2][kWarps][32 * N];   // each warp's map: A,
-    float H[2][kWarps][32 * N];   // and H, then in its place the state that enters the warp's rows
-    float R[BACKWARD ? 2 : 1][BACKWARD ? kWarps : 1][32 * N];  // backward: the map A mu + R, then the mu that enters
+    using V = typename Word<T>::V;
+    V A[2][kWarps][32];  // each warp's map: A,
+    V H[2][kWarps][32];  // and H, then in its place the state that enters the warp's rows
+    V R[BACKWARD ? 2 : 1][BACKWARD ? kWarps : 1][32];  // backward: the map A mu + R, then the mu that enters
     uint64_t full[kMostJobs], empty[kMostJobs];  // a tile is known, and by TMA its rows are there; is done with
     uint64_t mapped[2], entered[2];          // a tile's maps are there; its states
     Job job[kMostJobs];
@@ -434,7 +436,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int s = k % kStages, q = k % kJobs;
       if (k >= kJobs && !wait(&sc.empty[q], k / kJobs - 1)) break;
-      const Job job{more ? t : -1, int(len), at};
+      Job job{more ? t : -1, int(len), at.col, at.i, at.b, {0, 0}};
+      if (more) {
+        const int64_t c = at.col * 32 * N;
+        if (BACKWARD) {
+          job.out[0] = at.b * p.dxs[0] + t0 * p.dxs[1] + c;
+          job.out[1] = at.b * p.dgs[0] + t0 * p.dgs[1] + c;
+        } else {
+          job.out[0] = at.b * p.hs[0] + t0 * p.hs[1] + c;
+        }
+      }
       if (lane == 0) sc.job[q] = job;
       __syncwarp();
       if (lane == 0) {
@@ -466,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Job job = sc.job[k % kJobs];
       const int t = job.t;
       if (t < 0) return;
-      const Place at = job.at;
+      const Place at{job.b, job.col, job.i};
       const int64_t len = job.len;
       const int last = int((len - 1) / kTile);
       const int before = BACKWARD ? last - at.i : at.i;
@@ -487,30 +498,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           h[v] = c + v < p.D ? __ldg(p.saved + (int64_t(at.b) * p.kept + at.i * (kTile / kSave)) * p.D + c + v) : 0.f;
         if (!wait(&sc.mapped[par], k / 2)) return;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w)
+        for (int w = 0; w < kWarps; ++w) {
+          const V a = sc.A[par][w][lane], b = sc.H[par][w][lane];
+          sc.H[par][w][lane] = V::of(h);
 #pragma unroll
-          for (int v = 0; v < N; ++v) {
-            const float enters = h[v];
-            h[v] = apply(sc.A[par][w][lane * N + v], sc.H[par][w][lane * N + v], h[v]);
-            sc.H[par][w][lane * N + v] = enters;
-          }
+          for (int v = 0; v < N; ++v) h[v] = apply(a[v], b[v], h[v]);
+        }
       } else if (!wait(&sc.mapped[par], k / 2)) {
         return;
       }
       // the tile's map: the warps' maps in the order of the chain
-      const float(*const mapA)[32 * N] = sc.A[par];
-      float(*const mapH)[32 * N] = BACKWARD ? sc.R[BACKWARD ? par : 0] : sc.H[par];
+      const V(*const mapA)[32] = sc.A[par];
+      V(*const mapH)[32] = BACKWARD ? sc.R[BACKWARD ? par : 0] : sc.H[par];
 #pragma unroll
       for (int v = 0; v < N; ++v) A[v] = 1.f, H[v] = 0.f;
 #pragma unroll
-      for (int j = 0; j < kWarps; ++j)
+      for (int j = 0; j < kWarps; ++j) {
+        const int w = BACKWARD ? kWarps - 1 - j : j;
+        const V a = mapA[w][lane], b = mapH[w][lane];
 #pragma unroll
         for (int v = 0; v < N; ++v) {
-          const int w = BACKWARD ? kWarps - 1 - j : j;
-          const float a = mapA[w][lane * N + v];
-          H[v] = apply(a, mapH[w][lane * N + v], H[v]);
-          A[v] *= a;
+          H[v] = apply(a[v], b[v], H[v]);
+          A[v] *= a[v];
         }
+      }
       if (before > 0) {
         if (wanted) publish_map<N>(p, t, A, H);
         look_back<N>(p, t, before, step, st);
@@ -522,14 +533,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int j = 0; j < kWarps; ++j) {
         const int w = BACKWARD ? kWarps - 1 - j : j;
+        const V a = mapA[w][lane], b = mapH[w][lane];
+        mapH[w][lane] = V::of(st);
 #pragma unroll
         for (int v = 0; v < N; ++v) {
-          const float h = mapH[w][lane * N + v];
-          mapH[w][lane * N + v] = st[v];
           if (!BACKWARD && w * kRows % kSave == 0 && p.saved && c + v < p.D &&
               int64_t(at.i) * kTile + w * kRows < len)
             p.saved[(int64_t(at.b) * p.kept + at.i * (kTile / kSave) + w * kRows / kSave) * p.D + c + v] = st[v];
-          st[v] = apply(mapA[w][lane * N + v], h, st[v]);
+          st[v] = apply(a[v], b[v], st[v]);
         }
       }
       __syncwarp();
@@ -564,12 +575,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Job job = sc.job[fetched % kJobs];
       more = job.t >= 0;
       if (more) {
-        const int c = (job.at.col * 32 + lane) * N;
-        const int64_t t0 = int64_t(job.at.i) * kTile + warp * kRows;
+        const int c = (job.col * 32 + lane) * N;
+        const int64_t t0 = int64_t(job.i) * kTile + warp * kRows;
         uint8_t* const to = stages + s * S::kStageBytes + warp * kRows * kRowBytes;
-        fetch<T, kRows>(p, p.g, p.gs, job.at.b, c, t0, job.len, to);
-        fetch<T, kRows>(p, p.x, p.xs, job.at.b, c, t0, job.len, to + S::kBox);
-        if (BACKWARD) fetch<T, kRows>(p, p.dh, p.dhs, job.at.b, c, t0, job.len, to + 2 * S::kBox);
+        fetch<T, kRows>(p, p.g, p.gs, job.b, c, t0, job.len, to);
+        fetch<T, kRows>(p, p.x, p.xs, job.b, c, t0, job.len, to + S::kBox);
+        if (BACKWARD) fetch<T, kRows>(p, p.dh, p.dhs, job.b, c, t0, job.len, to + 2 * S::kBox);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -579,23 +590,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!TMA)
     for (int s = 0; s < kStages - 2; ++s)
       if (!fetch_own()) return;
+  // this warp's and lane's place in the outputs' tiles
+  const int64_t mine0 = BACKWARD ? (warp * kRows + kRows - 1) * p.dxs[1] + lane * N : warp * kRows * p.hs[1] + lane * N;
+  const int64_t mine1 = BACKWARD ? (warp * kRows + kRows - 1) * p.dgs[1] + lane * N : 0;
+  struct Turn {  // a tile's stage and place in the ring of jobs, and the ring's round
+    int stage = 0, job = 0, round = 0;
+    __device__ __forceinline__ void next() {
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      if (++job == kJobs) job = 0, ++round;
+    }
+  } ahead, here;
   Job cur{};
   cur.t = -1;
   for (int k = -1;; ++k) {
     Job next{};
     next.t = -1;
     if (k < 0 || cur.t >= 0) {
-      const int s = (k + 1) % kStages, par = (k + 1) & 1;
+      const int par = (k + 1) & 1;
       if (!TMA && !fetch_own()) return;  // tile k + kStages - 1
-      if (!wait(&sc.full[(k + 1) % kJobs], (k + 1) / kJobs)) return;
+      if (!wait(&sc.full[ahead.job], ahead.round)) return;
       if (!TMA) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");  // tile k + 1 is there
         __syncwarp();
       }
-      next = sc.job[(k + 1) % kJobs];
+      next = sc.job[ahead.job];
       if (next.t >= 0) {
-        const int left = next.len - (next.at.i * kTile + warp * kRows);
-        const uint8_t* const stage = stages + s * S::kStageBytes;
+        const int left = next.len - (next.i * kTile + warp * kRows);
+        const uint8_t* const stage = stages + ahead.stage * S::kStageBytes;
         auto word = [&](int tensor, int r) {
           return W::open(*reinterpret_cast<const uint32_t*>(stage + tensor * S::kBox + (r & ~7) * kRowBytes +
                                                             (r & 7) * kRowBytes + swizzle[r & 7]));
@@ -617,37 +638,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int r = 0; r < kRows; ++r)
             if (r < left) token(r);
         }
-#pragma unroll
-        for (int v = 0; v < N; ++v) {
-          sc.A[par][warp][lane * N + v] = A[v];
-          sc.H[par][warp][lane * N + v] = H[v];
-          if (BACKWARD) sc.R[par][warp][lane * N + v] = R[v];
-        }
+        sc.A[par][warp][lane] = A;
+        sc.H[par][warp][lane] = H;
+        if constexpr (BACKWARD) sc.R[par][warp][lane] = R;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sc.mapped[par]);
       }
     }
     if (k >= 0) {
       if (cur.t < 0) return;
-      const int s = k % kStages, par = k & 1;
-      const int64_t t0 = int64_t(cur.at.i) * kTile + warp * kRows;
-      const int b = cur.at.b;
-      const int left = int(cur.len - t0);
-      const int c = (cur.at.col * 32 + lane) * N;
+      const int par = k & 1;
+      const int left = cur.len - (cur.i * kTile + warp * kRows);
+      const int c = (cur.col * 32 + lane) * N;
       // every row and channel of this warp's part is there, and takes 4-byte stores
-      const bool whole = left >= kRows && (cur.at.col + 1) * 32 * N <= p.D && (N == 1 || p.wide);
-      const uint8_t* const stage = stages + s * S::kStageBytes;
+      const bool whole = left >= kRows && (cur.col + 1) * 32 * N <= p.D && (N == 1 || p.wide);
+      const uint8_t* const stage = stages + here.stage * S::kStageBytes;
       auto word = [&](int tensor, int r) {
         return W::open(*reinterpret_cast<const uint32_t*>(stage + tensor * S::kBox + (r & ~7) * kRowBytes +
                                                           (r & 7) * kRowBytes + swizzle[r & 7]));
       };
-      if (!wait(&sc.entered[par], k / 2)) return;
-      float in[N];
-#pragma unroll
-      for (int v = 0; v < N; ++v) in[v] = sc.H[par][warp][lane * N + v];
-      V st = W::make(in);
+      if (!wait(&sc.entered[par], k >> 1)) return;
+      V st = sc.H[par][warp][lane];
       if constexpr (!BACKWARD) {
-        T* to = static_cast<T*>(p.h) + b * p.hs[0] + t0 * p.hs[1] + c;
+        T* to = static_cast<T*>(p.h) + cur.out[0] + mine0;
         auto token = [&](int r) {
           const V g = word(0, r), x = word(1, r);
           V a, rest;
@@ -677,12 +690,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           d[r] = INPUT == TTT_SCAN_COMPLEMENT ? sub_(st, x) : st;
           st = fma_(a[r], st, INPUT == TTT_SCAN_COMPLEMENT ? mul_(rest[r], x) : x);
         }
-#pragma unroll
-        for (int v = 0; v < N; ++v) in[v] = sc.R[par][warp][lane * N + v];
-        V mu = W::make(in);
-        T* dx = static_cast<T*>(p.dx) + b * p.dxs[0] + t0 * p.dxs[1] + c;
-        T* dg = static_cast<T*>(p.dg) + b * p.dgs[0] + t0 * p.dgs[1] + c;
-        dx += (kRows - 1) * p.dxs[1], dg += (kRows - 1) * p.dgs[1];
+        V mu = sc.R[par][warp][lane];
+        T* dx = static_cast<T*>(p.dx) + cur.out[0] + mine0;  // the last row
+        T* dg = static_cast<T*>(p.dg) + cur.out[1] + mine1;
         if (whole) {
 #pragma unroll
           for (int r = kRows - 1; r >= 0; --r, dx -= p.dxs[1], dg -= p.dgs[1]) {
@@ -705,8 +715,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sc.empty[k % kJobs]);
+      if (lane == 0) mbar_arrive(&sc.empty[here.job]);
     }
+    here = ahead;
+    ahead.next();
     cur = next;
   }
 }
