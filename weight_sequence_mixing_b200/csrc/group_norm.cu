@@ -4,14 +4,21 @@
 // entry.  sum x^2 - n mean^2 would lose the digits of a group whose mean is large, and the
 // sum of squares about the mean takes a second pass over the data.  So runs of at most 32
 // tokens are summed about their own first value, which a run's spread is never far
-// below, and the (count, mean, sum of squares about it) of two parts are joined by
-//   mean = (n1 mean1 + n2 mean2) / n,   S = S1 + S2 + (mean2 - mean1)^2 n1 n2 / n
-// (Chan, Golub, LeVeque 1979), in an order that is fixed by the sizes alone.
+// below, and parts (count n_k, mean_k, S_k the sum of squares about it) are
+// joined by
+//   mean = sum n_k mean_k / n,   S = sum S_k + n_k (mean_k - mean)^2
+// (two at a time: Chan, Golub, LeVeque 1979), in an order that is fixed by the sizes alone.
 //
-// Two forms.  Where a group of a batch entry fits in shared memory, one block does all of
-// it.  Else a first kernel forms the statistics of (token range, channel) blocks and a
-// second joins them and normalises; both are bound by HBM, with x read twice where L2
+// Two forms.  A small group (16384 values at most, of a small tensor) is one block's, in
+// shared memory.  Else a first kernel forms the statistics of (token range, channel) blocks
+// and a second, launched behind it, joins them and normalises: x is read twice where L2
 // does not keep it (the second kernel walks backwards, from what was read last).
+//
+// Measured, SiLU, bf16: 1048576 tokens x 128 channels in 32 groups, statistics 50 us (82% of
+// the copy bandwidth), application 119 us (69%; the exponentials and reciprocals keep their
+// unit 57% busy, and a reciprocal shared by two values or an exponential from the FMA pipe
+// gained 2%), backward sums 123 us (67%) and dx 147 us (84%).  8 x 6084 tokens of 6 heads of
+// 64 (in L2): 10 and 19 us.
 #include <cmath>
 #include <algorithm>
 #include <new>

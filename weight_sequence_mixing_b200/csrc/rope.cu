@@ -41,6 +41,9 @@ struct RopeArgs {
   int64_t row_tiles;            // of tokens
 };
 
+// tokens of a thread: eight or four steps in all, of which a head takes one
+constexpr int tokens_of(int bytes, bool one, int heads) { return std::max(1, (one || bytes < 16 ? 8 : 4) / heads); }
+
 // A thread owns a vector of pairs (or of channels that are only copied) of every token: its
 // frequencies stay in registers while it walks over tiles of (token, head) steps.  Of a
 // tile it first issues all loads, then forms each token's angles once for its HEADS heads,
@@ -49,11 +52,8 @@ struct RopeArgs {
 //   ONE: the two channels of a pair lie in one vector (interleaved); else in two.
 // bf16 takes the hardware's sine and cosine (2^-21.2 off on [-pi, pi], far below the
 // output's 2^-9), fp32 sincospif.
-// Measured against this (196608 tokens x 2 heads x 512 bf16, 139 us; the copy of as many bytes 123): angles in fp64 and
-// one (token, heads) step ahead, 200 us; angles of a tile shared in shared memory, 211 us.
-// tokens of a thread: eight or four steps in all, of which a head takes one
-constexpr int tokens_of(int bytes, bool one, int heads) { return std::max(1, (one || bytes < 16 ? 8 : 4) / heads); }
-
+// Measured: 196608 tokens x 2 heads x 512 bf16 139 us (88% of the copy bandwidth).  Angles in
+// fp64, one (token, heads) step ahead, took 200 us; a tile's angles shared in shared memory 211.
 template <class T, int BYTES, bool ONE, int HEADS, bool POS_F32>
 __global__ void __launch_bounds__(256, ONE ? 3 : 2)
     rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopeTable tab) {

@@ -10,15 +10,18 @@
 // earlier tile whose outgoing state is known, applies the maps in between in token order,
 // and publishes its own outgoing state.  Every input is read once and every output
 // written once: the bound is HBM.
-//   - A block's warps have three trades.  One fetches the rows of the tiles to come into
-//     a ring of stages (TMA; rows that TMA cannot address, on strides that are no multiple
-//     of 16 bytes, by 4-byte asynchronous copies or plain loads).  Eight sweep a tile's
-//     rows twice: first for the maps, and one tile later, when the states that enter are
-//     there, for the states themselves.  Two follow the chain of states from tile to tile, the block's tiles in turn.
-//     (Without TMA the sweeping warps fetch their own rows.)  So a tile's state is waited for while the next tile's maps are formed, and loads run
-//     on throughout.  The gates are formed in both sweeps: keeping them (8 bytes a value
-//     in registers) was measured, and it holds too few tokens in flight for the chain's
-//     latency (scene layer of 1029120 tokens, 1024 channels: 5.98 ms, against 1.74 here).
+//   - A block's warps have three trades.  One hands out tiles and fetches their rows into a
+//     ring of stages by TMA.  Sixteen sweep a tile's rows twice: first for the maps, and one
+//     tile later, when the states that enter are there, for the states themselves.  Two
+//     follow the chain of states from tile to tile, the block's tiles in turn.  So a tile's
+//     state is waited for while the next tile's maps are formed, and loads run on
+//     throughout.  (Rows that TMA cannot address, on strides that are no multiple of 16
+//     bytes, are fetched by the sweeping warps, by 4-byte asynchronous copies or, on odd
+//     2-byte strides, plain loads.)
+//   - The gates are formed in both sweeps.  Keeping them (8 bytes a value in registers) was
+//     measured: it holds too few tokens in flight for the chain's latency (5.98 ms).
+//   - A published map or state is a word that shows by itself whether it is there.  Flags
+//     behind fences took 7.0 ms in the same form.
 //   - A warp takes the same channels of a few consecutive tokens; a lane one 4-byte word
 //     of channels of each.
 //   - Tiles are handed out by a counter, tokens first to last, so a tile only waits for
@@ -29,6 +32,13 @@
 // The backward pass is the same over the tokens last to first; the states h_{t-1} that the
 // gates' gradient needs are formed again in fp32 from states that the forward pass kept
 // (one in 64 tokens), not read back rounded.
+//
+// Measured, bf16, 1024 channels: forward over 1029120 tokens 1.26 ms (77% of the copy
+// bandwidth; exponential gate), over 64 sequences of 2048 140 us (88%; plain gate), 181 us
+// with a sigmoid and its complement, where the exponentials and reciprocals keep their unit
+// 69% busy; backward 262 and 300 us (78 and 68%), bound by issue.  A single long chain adds
+// its latency: 131072 tokens take 167 us forward and 313 back.  Tiles half as long, two
+// blocks an SM, took 1.74 ms for the million tokens; one chain warp 2.30 (at that length).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
