@@ -746,10 +746,11 @@ __global__ void __launch_bounds__(kSmallThreads) norm_small_grad_kernel(const __
       }
     }
   q = block_sum(q, part);
-  for (int c = threadIdx.x; c < p.n; c += kSmallThreads) {
-    float2 s = sums[c];
-    for (int r = 1; r < p.rows; ++r) s.x += sums[r * p.n + c].x, s.y += sums[r * p.n + c].y;
-    p.channel_sums[int64_t(b) * p.C + g * p.n + c] = s;
+  for (int c = threadIdx.x / 32; c < p.n; c += kSmallThreads / 32) {  // a warp a channel
+    float2 s = make_float2(0.f, 0.f);
+    for (int r = threadIdx.x % 32; r < p.rows; r += 32) s.x += sums[r * p.n + c].x, s.y += sums[r * p.n + c].y;
+    s = make_float2(warp_sum(s.x), warp_sum(s.y));
+    if (threadIdx.x % 32 == 0) p.channel_sums[int64_t(b) * p.C + g * p.n + c] = s;
   }
   const float count = float(p.N) * float(p.n), m0 = q.x / count, m1 = q.y / count;
   for (int i = lane * V; i < p.n; i += p.lanes * V) {
@@ -873,7 +874,7 @@ template <class T, int BYTES, int ACT>
 int launch_act(bool backward, NormArgs& a, const Cut& k, cudaStream_t st) {
   constexpr int V = BYTES / int(sizeof(T));
   if (k.small) return launch_small<T, BYTES, ACT>(backward, a, k, st);
-  if constexpr (BYTES == 16) {
+  if constexpr (V >= 4) {
     if (a.n % V == 0) return launch_blocks<T, BYTES, V, ACT>(backward, a, k, st);
     if constexpr (V == 8)
       if (a.n % 4 == 0) return launch_blocks<T, BYTES, 4, ACT>(backward, a, k, st);
@@ -889,18 +890,17 @@ int launch(bool backward, int act, NormArgs& a, const Cut& k, cudaStream_t st) {
   }
 }
 
-// Vectors of 16 or 4 bytes or of one channel: the widest that all rows start on and that
+// Vectors of 16, 8 or 4 bytes or of one channel: the widest that all rows start on and that
 // groups (where they lie apart, or each has a block of its own) or rows are whole numbers of.
 int vector_bytes(const RowTensor* t, int nt, const ttt_strides* const* s, int C, int n, int elem, bool each) {
   int wide = 16;
-  const auto narrower = [&] { wide = wide == 16 ? 4 : elem; };
   for (int i = 0; i < nt; ++i) {
     const bool together = s[i]->head == n || n == C;  // a row's groups follow one another
-    while (wide > elem && (C * elem % wide || ((!together || each) && n * elem % wide))) narrower();
+    while (wide > elem && (C * elem % wide || ((!together || each) && n * elem % wide))) wide /= 2;
     // channels last: rows are aligned by their first group
     RowTensor rows = t[i];
     if (together) rows.n[1] = 1;
-    while (wide > elem && !rows_aligned(rows, wide)) narrower();
+    while (wide > elem && !rows_aligned(rows, wide)) wide /= 2;
   }
   return wide;
 }
@@ -949,7 +949,7 @@ size_t space_needed(const ttt_norm* h, int32_t B, int64_t N, bool backward) {
   const int elem = c.dtype == TTT_BF16 ? 2 : 4;
   if (fits_small(B, N, c.C, c.C / c.groups, backward)) return workspace_of(cut_small(N, 1, 1, backward), B, c.C, backward);
   size_t most = 0;
-  for (int wide : {16, 4, elem})
+  for (int wide = 16; wide >= elem; wide /= 2)
     if (c.C * elem % wide == 0)
       most = std::max(most, workspace_of(cut_blocks(B, N, c.C, c.groups, wide / elem, backward), B, c.C, backward));
   return most;
@@ -969,9 +969,12 @@ int run(const ttt_norm* h, bool backward, NormArgs& a, const RowTensor* t, const
   a.parts = a.channel_sums + (backward ? size_t(a.B) * k.row_blocks * c.C : 0);
   if (elem == 2)
     return wide == 16  ? launch<__nv_bfloat16, 16>(backward, c.act, a, k, st)
+           : wide == 8 ? launch<__nv_bfloat16, 8>(backward, c.act, a, k, st)
            : wide == 4 ? launch<__nv_bfloat16, 4>(backward, c.act, a, k, st)
                        : launch<__nv_bfloat16, 2>(backward, c.act, a, k, st);
-  return wide == 16 ? launch<float, 16>(backward, c.act, a, k, st) : launch<float, 4>(backward, c.act, a, k, st);
+  return wide == 16  ? launch<float, 16>(backward, c.act, a, k, st)
+         : wide == 8 ? launch<float, 8>(backward, c.act, a, k, st)
+                     : launch<float, 4>(backward, c.act, a, k, st);
 }
 
 }  // namespace
