@@ -343,7 +343,7 @@ def _dot64(d, key, v):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("D,wide", [(70, 144), (72, 144), (33, 64), (1, 8), (9, 9)])
+@pytest.mark.parametrize("D,wide", [(70, 144), (72, 144), (33, 64), (1, 8), (9, 9), (131, 131), (193, 195), (127, 256)])
 def test_scan_rows_of_any_width_and_stride(dtype, D, wide):
     """Channels that are no whole number of a tile's columns, in rows that start on 16 bytes, on 4 or on 2."""
     case = (2, 600, D, "exp", "complement", dtype, True, True, False)

@@ -16,8 +16,9 @@
 //     follow the chain of states from tile to tile, the block's tiles in turn.  So a tile's
 //     state is waited for while the next tile's maps are formed, and loads run on
 //     throughout.  (Rows that TMA cannot address, on strides that are no multiple of 16
-//     bytes, are fetched by the sweeping warps, by 4-byte asynchronous copies or, on odd
-//     2-byte strides, plain loads.)
+//     bytes, are fetched by the sweeping warps in 4-byte asynchronous copies.  A row that
+//     starts on an odd multiple of 2 bytes is copied from the 2 bytes before it on, and
+//     shifted where it is read.)
 //   - The gates are formed in both sweeps.  Keeping them (8 bytes a value in registers) was
 //     measured: it holds too few tokens in flight for the chain's latency (5.98 ms).
 //   - A published map or state is a word that shows by itself whether it is there.  Flags
@@ -316,6 +317,36 @@ __device__ __forceinline__ void put_word(const ScanArgs& p, T* to, int c, typena
   }
 }
 
+// A row of one output by a warp, a lane's word at channel c.  Where the row starts on an odd
+// multiple of 2 bytes, the words of memory are those one channel earlier: the second half of
+// the lane before and the first of one's own.
+template <class T>
+__device__ __forceinline__ void put_row(const ScanArgs& p, T* to, int c, typename Word<T>::V v) {
+  const uint32_t w = Word<T>::close(v);
+  if (Word<T>::N == 1 || p.wide) {
+    if (c < p.D) *reinterpret_cast<uint32_t*>(to) = w;
+    return;
+  }
+  uint16_t* const h = reinterpret_cast<uint16_t*>(to);
+  if ((reinterpret_cast<uintptr_t>(to) & 2) == 0) {
+    if (c + 1 < p.D)
+      *reinterpret_cast<uint32_t*>(to) = w;
+    else if (c < p.D)
+      h[0] = uint16_t(w);
+    return;
+  }
+  const int lane = threadIdx.x % 32;
+  const uint32_t before = __shfl_up_sync(~0u, w, 1);
+  if (lane == 0) {
+    if (c < p.D) h[0] = uint16_t(w);
+  } else if (c < p.D) {
+    *reinterpret_cast<uint32_t*>(h - 1) = before >> 16 | w << 16;
+  } else if (c == p.D) {
+    h[-1] = uint16_t(before >> 16);
+  }
+  if (lane == 31 && c + 1 < p.D) h[1] = uint16_t(w >> 16);
+}
+
 // Tiles of 256 tokens forward and 128 backward (one tensor more), three and four stages:
 // 192 KB, one block an SM.
 template <class T, bool BACKWARD>
@@ -336,39 +367,54 @@ struct Shape {
     uint64_t full[kMostJobs], empty[kMostJobs];  // a tile is known, and by TMA its rows are there; is done with
     uint64_t mapped[2], entered[2];          // a tile's maps are there; its states
     Job job[kMostJobs];
+    uint32_t extra[N == 2 ? kStages : 1][kTensors][kTile];  // see fetch
     int abort;
   };
   static constexpr int kSmem = 1024 + kStages * kStageBytes + int(sizeof(Scratch));
 };
 
 // A warp's rows of one tensor's tile, from token t0 on, into shared memory at the swizzle TMA
-// uses.  Nothing is read where the size is 0: the word is filled with zero.
+// uses.  Only the bytes of live channels are read, the rest of a word is filled with zero.
+// Rows on odd multiples of 2 bytes (kLoad2): a lane's word starts one channel early, and the
+// channel that this leaves out of the last lane's goes to `extra`, one word a row.
 template <class T, int ROWS>
-__device__ __forceinline__ void fetch(const ScanArgs& p, const void* base, const int64_t (&s)[2], int b, int c, int64_t t0,
-                                      int64_t len, uint8_t* dst) {
-  const int lane = threadIdx.x % 32;
-  const int rows = c < p.D ? int(len - t0 >= ROWS ? ROWS : len > t0 ? len - t0 : 0) : 0;
-  const T* from = static_cast<const T*>(base) + (rows ? b * s[0] + t0 * s[1] + c : 0);
+__device__ __forceinline__ void fetch(const ScanArgs& p, const void* base, const int64_t (&s)[2], int b, int c0, int64_t t0,
+                                      int64_t len, uint8_t* dst, uint32_t* extra) {
+  const int lane = threadIdx.x % 32, c = c0 + lane * Word<T>::N;
+  const int rows = int(len - t0 >= ROWS ? ROWS : len > t0 ? len - t0 : 0);
+  const T* from = static_cast<const T*>(base) + (rows ? b * s[0] + t0 * s[1] : 0);
   const uint32_t to = smem_u32(dst);
   if (p.load == kLoad4) {
+    from += c < p.D ? c : 0;
 #pragma unroll 16
     for (int r = 0; r < ROWS; ++r) {
       asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + r * kRowBytes + ((lane * 4) ^ ((r & 7) << 4))),
-                   "l"(from), "r"(r < rows ? 4 : 0)
+                   "l"(from), "r"(r < rows && c < p.D ? 4 : 0)
                    : "memory");
       if (r + 1 < rows) from += s[1];
     }
-  } else {
-#pragma unroll 16
-    for (int r = 0; r < ROWS; ++r) {
-      uint32_t w = 0;
-      if (r < rows) {
-        const uint16_t* h = reinterpret_cast<const uint16_t*>(from);
-        w = h[0];
-        if (Word<T>::N == 2 && c + 1 < p.D) w |= uint32_t(h[1]) << 16;
-      }
-      if (r + 1 < rows) from += s[1];
-      *reinterpret_cast<uint32_t*>(dst + r * kRowBytes + ((lane * 4) ^ ((r & 7) << 4))) = w;
+    return;
+  }
+  // bytes of the word that starts at channel f: of two channels, one or none
+  auto live = [&](int f) { return f >= p.D ? 0 : f + 1 >= p.D ? 2 : 4; };
+#pragma unroll 4
+  for (int r = 0; r < rows; ++r, from += s[1]) {
+    const int late = int(reinterpret_cast<uintptr_t>(from) >> 1 & 1);
+    const int f = c - late, n = live(f);
+    const uint32_t word = to + r * kRowBytes + ((lane * 4) ^ ((r & 7) << 4));
+    if (f < 0 && from == static_cast<const T*>(base)) {  // nothing lies before a tensor's first element
+      *reinterpret_cast<uint32_t*>(dst + r * kRowBytes + ((lane * 4) ^ ((r & 7) << 4))) =
+          uint32_t(*reinterpret_cast<const uint16_t*>(from)) << 16;
+    } else {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(word),
+                   "l"(reinterpret_cast<uintptr_t>(n ? from + f : from) & ~uintptr_t(3)), "r"(n)
+                   : "memory");
+    }
+    if (late && lane == 31) {
+      const int e = c0 + 63, m = live(e);
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(extra + r)),
+                   "l"(reinterpret_cast<uintptr_t>(m ? from + e : from) & ~uintptr_t(3)), "r"(m)
+                   : "memory");
     }
   }
 }
@@ -585,12 +631,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Job job = sc.job[fetched % kJobs];
       more = job.t >= 0;
       if (more) {
-        const int c = (job.col * 32 + lane) * N;
-        const int64_t t0 = int64_t(job.i) * kTile + warp * kRows;
-        uint8_t* const to = stages + s * S::kStageBytes + warp * kRows * kRowBytes;
-        fetch<T, kRows>(p, p.g, p.gs, job.b, c, t0, job.len, to);
-        fetch<T, kRows>(p, p.x, p.xs, job.b, c, t0, job.len, to + S::kBox);
-        if (BACKWARD) fetch<T, kRows>(p, p.dh, p.dhs, job.b, c, t0, job.len, to + 2 * S::kBox);
+        const int c0 = job.col * 32 * N, first = warp * kRows;
+        const int64_t t0 = int64_t(job.i) * kTile + first;
+        uint8_t* const to = stages + s * S::kStageBytes + first * kRowBytes;
+        auto& extra = sc.extra[N == 2 ? s : 0];
+        fetch<T, kRows>(p, p.g, p.gs, job.b, c0, t0, job.len, to, extra[0] + first);
+        fetch<T, kRows>(p, p.x, p.xs, job.b, c0, t0, job.len, to + S::kBox, extra[1] + first);
+        if constexpr (BACKWARD) fetch<T, kRows>(p, p.dh, p.dhs, job.b, c0, t0, job.len, to + 2 * S::kBox, extra[2] + first);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -600,6 +647,37 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!TMA)
     for (int s = 0; s < kStages - 2; ++s)
       if (!fetch_own()) return;
+  // the lane's word of row r (of this warp's) of a tile's tensor
+  struct Rows {
+    const uint8_t* stage;
+    const uint32_t* extra;   // rows on odd multiples of 2 bytes (kLoad2): see fetch
+    unsigned late, alternate;  // by tensor: whether row 0 starts so, and whether rows take turns
+  };
+  auto rows_of = [&](int stage, const Job& job) {
+    Rows rows{stages + stage * S::kStageBytes, nullptr, 0u, 0u};
+    if (!TMA && N == 2 && p.load == kLoad2) {
+      rows.extra = sc.extra[N == 2 ? stage : 0][0] + warp * kRows;
+      const int t0 = job.i * kTile + warp * kRows;
+      auto parity = [&](const void* base, const int64_t(&s)[2]) {
+        return unsigned(reinterpret_cast<uintptr_t>(base) >> 1) + unsigned(job.b) * unsigned(s[0]) + unsigned(t0) * unsigned(s[1]);
+      };
+      rows.late = (parity(p.g, p.gs) & 1) | (parity(p.x, p.xs) & 1) << 1 | (BACKWARD ? (parity(p.dh, p.dhs) & 1) << 2 : 0);
+      rows.alternate = unsigned(p.gs[1] & 1) | unsigned(p.xs[1] & 1) << 1 | (BACKWARD ? unsigned(p.dhs[1] & 1) << 2 : 0);
+    }
+    return rows;
+  };
+  auto word_of = [&](const Rows& rows, int tensor, int r) {
+    const uint8_t* const row = rows.stage + tensor * S::kBox + r * kRowBytes;
+    uint32_t w = *reinterpret_cast<const uint32_t*>(row + swizzle[r & 7]);
+    if (!TMA && N == 2 && rows.extra) {
+      if ((rows.late ^ (r & 1 ? rows.alternate : 0u)) >> tensor & 1) {
+        const uint8_t* const next = row + warp * kRows * kRowBytes + (((lane + 1) * 4) ^ ((r & 7) << 4));
+        const uint32_t v = lane == 31 ? rows.extra[tensor * kTile + r] : *reinterpret_cast<const uint32_t*>(next);
+        w = __byte_perm(w, v, 0x5432);
+      }
+    }
+    return W::open(w);
+  };
   // this warp's and lane's place in the outputs' tiles
   const int64_t mine0 = BACKWARD ? (warp * kRows + kRows - 1) * p.dxs[1] + lane * N : warp * kRows * p.hs[1] + lane * N;
   const int64_t mine1 = BACKWARD ? (warp * kRows + kRows - 1) * p.dgs[1] + lane * N : 0;
@@ -626,11 +704,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       next = sc.job[ahead.job];
       if (next.t >= 0) {
         const int left = next.len - (next.i * kTile + warp * kRows);
-        const uint8_t* const stage = stages + ahead.stage * S::kStageBytes;
-        auto word = [&](int tensor, int r) {
-          return W::open(*reinterpret_cast<const uint32_t*>(stage + tensor * S::kBox + (r & ~7) * kRowBytes +
-                                                            (r & 7) * kRowBytes + swizzle[r & 7]));
-        };
+        const Rows rows = rows_of(ahead.stage, next);
+        auto word = [&](int tensor, int r) { return word_of(rows, tensor, r); };
         V A = W::all(1.f), H = W::all(0.f), R = W::all(0.f);
         auto token = [&](int r) {
           const V g = word(0, r), x = word(1, r);
@@ -662,11 +737,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int c = (cur.col * 32 + lane) * N;
       // every row and channel of this warp's part is there, and takes 4-byte stores
       const bool whole = left >= kRows && (cur.col + 1) * 32 * N <= p.D && (N == 1 || p.wide);
-      const uint8_t* const stage = stages + here.stage * S::kStageBytes;
-      auto word = [&](int tensor, int r) {
-        return W::open(*reinterpret_cast<const uint32_t*>(stage + tensor * S::kBox + (r & ~7) * kRowBytes +
-                                                          (r & 7) * kRowBytes + swizzle[r & 7]));
-      };
+      const Rows rows = rows_of(here.stage, cur);
+      auto word = [&](int tensor, int r) { return word_of(rows, tensor, r); };
       if (!wait(&sc.entered[par], k >> 1)) return;
       V st = sc.H[par][warp][lane];
       if constexpr (!BACKWARD) {
@@ -687,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int r = 0; r < kRows; ++r, to += p.hs[1]) {
             token(r);
-            if (r < left && c < p.D) put_word<T>(p, to, c, st);
+            if (r < left) put_row<T>(p, to, c, st);
           }
         }
       } else {
@@ -717,10 +789,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (r < left) {
               const V lam = add_(word(2, r), mu);
               mu = mul_(a[r], lam);
-              if (c < p.D) {
-                put_word<T>(p, dx, c, INPUT == TTT_SCAN_COMPLEMENT ? mul_(rest[r], lam) : lam);
-                put_word<T>(p, dg, c, gate_grad<GATE>(a[r], rest[r], mul_(lam, d[r])));
-              }
+              put_row<T>(p, dx, c, INPUT == TTT_SCAN_COMPLEMENT ? mul_(rest[r], lam) : lam);
+              put_row<T>(p, dg, c, gate_grad<GATE>(a[r], rest[r], mul_(lam, d[r])));
             }
         }
       }
