@@ -210,3 +210,31 @@ def test_columns_of_one_buffer_that_share_an_element_are_refused():
     assert _forward(h, dict(a, h=64 * M + 254)) == binding.TTT_ERR_INVALID_ARG  # x's last column
     assert _forward(h, dict(a, h=64 * M + 258)) == binding.TTT_ERR_INVALID_ARG  # g's first, one token on
     binding.LIB.ttt_scan_destroy(h)
+
+
+def test_the_binding_refuses_what_is_not_on_its_device():
+    """Host checks of the native module, before any call of the library."""
+    import torch
+    binding, ops = _lib()
+    op = ops.RotaryPositions(dict(d=8, pairs=(4,), dtype="bf16"), device="cuda:0")
+    x, pos = torch.zeros((1, 1, 1, 8), dtype=torch.bfloat16), torch.zeros((1, 1), dtype=torch.int32)
+    with pytest.raises(ValueError, match="cuda:0"):
+        op.forward(x, pos)
+    with pytest.raises(ValueError, match="shape"):
+        op.forward(x[..., :4], pos)
+    with pytest.raises(ValueError, match="shape"):
+        op.forward(x.float(), pos)
+    with pytest.raises(TypeError):
+        op.forward([0.0] * 8, pos)
+    with pytest.raises(TypeError):
+        op.forward(x, None)
+    op.close()
+    op.close()
+    with pytest.raises(ValueError, match="closed"):
+        op.forward(x, pos)
+    with pytest.raises(binding.TTTError):
+        ops.RotaryPositions(dict(d=7, pairs=(4,), dtype="bf16"))
+    with pytest.raises(KeyError):
+        ops.RotaryPositions(dict(d=8, pairs=(4,), dtype="f16"))
+    with pytest.raises(ValueError):
+        ops.RotaryPositions(dict(d=8, pairs=(4,), dtype="bf16"), device="cpu")
