@@ -29,7 +29,9 @@
  *     a call that goes wrong on the device sets bits, and its outputs are then not to
  *     be used; no call clears them.  Bit 1 (value 2): a bounded device wait ran out
  *     (2 s, as in ttt.h).
- *   - Results do not depend on timing: the same call gives the same bits.
+ *   - Results do not depend on timing: the same call gives the same bits.  Rows that
+ *     start on other alignments or strides may take another kernel, of the same
+ *     definition and arithmetic, whose last bits may differ.
  */
 #ifndef TTT_OPS_H_
 #define TTT_OPS_H_

@@ -387,6 +387,31 @@ def test_scans_on_two_streams_at_once_and_a_broadcast_input():
         assert torch.equal(h, want[0]) and torch.equal(last, want[1])
 
 
+@pytest.mark.parametrize("dtype,L", [("bf16", 900), ("f32", 900), ("bf16", 3), ("bf16", 1)])
+def test_scan_with_one_decay_for_all_tokens(dtype, L):
+    """A gate per channel, broadcast over batch and tokens (strides 0): values and gradients of every token.  The
+    decay's own gradient is their sum, for the caller to take: dg has no place in the decay's row."""
+    from weight_sequence_mixing_b200.binding import TTTError
+    case = (3, L, 72, "sigmoid", "complement", dtype, True, L > 3, False)
+    d = _scan_inputs(case)
+    decay = d["g"][0, 0].clone()
+    d["g"] = decay.expand(3, L, 72).contiguous()
+    op = _ops().GatedScan(dict(D=72, gate="sigmoid", inp="complement", dtype=dtype))
+    g, x, dh = decay.cuda().expand(3, L, 72), d["x"].cuda(), d["dh"].cuda()
+    saved, n = op.new_saved(3, L), None if d["lengths"] is None else d["lengths"].cuda()
+
+    def run():
+        h, last = op.forward(g, x, h0=d["h0"].cuda(), lengths=n, saved=saved)
+        dg, dx, dh0 = op.backward(dh, g, x, saved, dh_last=d["dh_last"].cuda(), lengths=n)
+        op.check_status()
+        return dict(h=h, h_last=last, dg=dg, dx=dx, dh0=dh0)
+    got, again = run(), run()
+    _check_scan(case, d, got)
+    assert all(torch.equal(got[k], again[k]) for k in got)
+    with pytest.raises(TTTError):
+        op.backward(dh, g, x, saved, dg=torch.zeros(72, dtype=g.dtype, device="cuda").expand(3, L, 72))
+
+
 def test_many_short_sequences():
     """More batch entries than a grid has rows: one new token and a few of each."""
     B, D = 70001, 6
