@@ -259,38 +259,39 @@ __global__ void __launch_bounds__(kThreads, 3) norm_parts_kernel(const __grid_co
       v = {float((each + (r < more ? 1 : 0)) * Q), m.x, m.y};
     });
     if (lane == 0)
-      p.parts[((int64_t(b) * p.row_blocks + rb) * p.col_blocks + cb) * p.slots + g - g0] = make_float2(v.mean, v.S);
+      p.parts[((int64_t(b) * p.col_blocks + cb) * p.slots + g - g0) * p.row_blocks + rb] = make_float2(v.mean, v.S);
   }
 }
 
 // Where the blocks' parts of group g are, and how many values each is of.  Where all lie in
-// one block of channels (the usual case) they are a row apart and of `each` values, the last
-// of `end`.
+// one block of channels (the usual case) they follow one another and are of `each` values,
+// the last of `end`.  A group's parts lie together: a block that joins them reads whole lines
+// (1048576 x 128 bf16 in 32 groups: 444 parts a group, forward 187 us with a block's parts
+// together instead, 156 so).
 struct PartsOf {
   const NormArgs& p;
   const float2* parts;
-  int g, width, first, blocks, all, hop;
+  int g, width, first, blocks, all;
   float each, end;
   __device__ __forceinline__ PartsOf(const NormArgs& p, int b, int g, int V) : p(p), g(g), width(p.lanes * V) {
     first = g * p.n / width, blocks = ((g + 1) * p.n - 1) / width - first + 1;
     all = p.row_blocks * blocks;
-    hop = p.col_blocks * p.slots;
     each = float(p.range), end = float(p.N - int64_t(p.row_blocks - 1) * p.range);
-    parts = p.parts + int64_t(b) * p.row_blocks * hop;
+    parts = p.parts + int64_t(b) * p.col_blocks * p.slots * p.row_blocks;
     if (blocks == 1) {
       each *= float(p.n), end *= float(p.n);
-      parts += first * p.slots + g - first * width / p.n;
+      parts += int64_t(first * p.slots + g - first * width / p.n) * p.row_blocks;
     }
   }
   __device__ __forceinline__ float2 at(int e, float* values) const {
     if (blocks == 1) {
       *values = e == all - 1 ? end : each;
-      return parts[int64_t(e) * hop];
+      return parts[e];
     }
     const int rb = e / blocks, cb = first + e - rb * blocks, c0 = cb * width;
     const float n = float(min((g + 1) * p.n, min(p.C, c0 + width)) - max(g * p.n, c0));
     *values = (rb == p.row_blocks - 1 ? end : each) * n;
-    return parts[int64_t(rb) * hop + cb * p.slots + g - c0 / p.n];
+    return parts[int64_t(cb * p.slots + g - c0 / p.n) * p.row_blocks + rb];
   }
 };
 
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_sums_kernel(const __grid_con
 #pragma unroll
     for (int m = 16; m; m /= 2) q0 += __shfl_xor_sync(~0u, q0, m), q1 += __shfl_xor_sync(~0u, q1, m);
     if (threadIdx.x % 32 == 0)
-      p.parts[((int64_t(b) * p.row_blocks + rb) * p.col_blocks + cb) * p.slots + g - g0] = make_float2(q0, q1);
+      p.parts[((int64_t(b) * p.col_blocks + cb) * p.slots + g - g0) * p.row_blocks + rb] = make_float2(q0, q1);
   }
 }
 
