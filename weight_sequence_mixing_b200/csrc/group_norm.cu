@@ -14,11 +14,10 @@
 // and a second, launched behind it, joins them and normalises: x is read twice where L2
 // does not keep it (the second kernel walks backwards, from what was read last).
 //
-// Measured, SiLU, bf16: 1048576 tokens x 128 channels in 32 groups, statistics 50 us (82% of
-// the copy bandwidth), application 119 us (69%; the exponentials and reciprocals keep their
-// unit 57% busy, and a reciprocal shared by two values or an exponential from the FMA pipe
-// gained 2%), backward sums 123 us (67%) and dx 147 us (84%).  8 x 6084 tokens of 6 heads of
-// 64 (in L2): 10 and 19 us.
+// Measured, SiLU, bf16: 2 x 1048576 tokens x 128 channels in 32 groups, statistics 83 us (98%
+// of the copy bandwidth), application 190 us (86%; a reciprocal shared by two values or an
+// exponential from the FMA pipe gained 2%), backward sums 183 us (90%) and dx 264 us (93%).
+// 8 x 6084 tokens of 6 heads of 64 (in L2): 10 and 19 us.
 #include <cmath>
 #include <algorithm>
 #include <new>
@@ -403,12 +402,27 @@ struct Known {
   }
 };
 
-// Backward, of one range of tokens and block of channels: each channel's sums of dz and dz xhat
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+  const uint32_t a = uint32_t(__cvta_generic_to_shared(to));
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(a), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(a), "l"(from), "n"(BYTES) : "memory");
+}
+// Backward, of one range of tokens and block of channels: each channel's sums of dz and dz xhat.
+// A thread's vectors of x and dy come through places of its own in shared memory, kAhead rows
+// ahead: the slope's arithmetic needs the registers that as many rows would take (2 x 1048576 x
+// 128, SiLU, bf16: backward 444 us, 494 with four rows at a time in registers).  Eight rows ahead
+// take 437 us there, but 277 instead of 219 in fp32 without an activation (2 x 262144 x 128).
+constexpr int kAhead = 4;
+template <int BYTES>
+constexpr int kRingBytes = BYTES >= 4 ? kAhead * 2 * kThreads * BYTES : 0;  // no asynchronous copy of 2 bytes
 template <class T, int BYTES, int Q, int ACT>
 __global__ void __launch_bounds__(kThreads, 2) norm_sums_kernel(const __grid_constant__ NormArgs p) {
   using X = Vec<T, BYTES>;
   using P = typename X::P;
-  constexpr int V = X::N, kPacks = X::kPacks, kStep = Q > P::N ? Q : P::N, kMeans = V / kStep, kAtOnce = 4;
+  constexpr int V = X::N, kPacks = X::kPacks, kStep = Q > P::N ? Q : P::N, kMeans = V / kStep;
   extern __shared__ float2 threads[];
   cudaTriggerProgrammaticLaunchCompletion();
   const int cb = blockIdx.x, rb = blockIdx.y, b = blockIdx.z;
@@ -426,40 +440,57 @@ __global__ void __launch_bounds__(kThreads, 2) norm_sums_kernel(const __grid_con
     const T* x = static_cast<const T*>(p.x) + k.at(p.xs, b) + (t0 + row) * p.xs[2];
     const T* dy = static_cast<const T*>(p.dy) + k.at(p.dys, b) + (t0 + row) * p.dys[2];
     const int64_t hop = p.rows * p.xs[2], dhop = p.rows * p.dys[2];
-    for (int left = tokens > row ? (tokens - row + p.rows - 1) / p.rows : 0; left > 0;) {
-      const int run = min(left, kRun);  // sums of runs, so that no long sum swallows its terms
+    const int mine = tokens > row ? (tokens - row + p.rows - 1) / p.rows : 0;
+    // row j's place is filled again a step after it was read
+    unsigned char* const ring = reinterpret_cast<unsigned char*>(threads + p.rows * width) + threadIdx.x * BYTES;
+    int next = 0;
+    auto fetch = [&] {
+      if constexpr (BYTES >= 4) {
+        if (next < mine) {
+          unsigned char* const to = ring + (next % kAhead) * (2 * kThreads * BYTES);
+          copy_async<BYTES>(to, x);
+          copy_async<BYTES>(to + kThreads * BYTES, dy);
+          x += hop;
+          dy += dhop;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        ++next;
+      }
+    };
+    for (int e = 0; e < kAhead - 1; ++e) fetch();
+    for (int j0 = 0; j0 < mine; j0 += kRun) {  // sums of runs, so that no long sum swallows its terms
       P s0[kPacks], s1[kPacks];
 #pragma unroll
       for (int i = 0; i < kPacks; ++i) s0[i] = s1[i] = P::all(0.f);
-      for (int j = 0; j < run; j += kAtOnce) {
-        X v[kAtOnce], d[kAtOnce];
-#pragma unroll
-        for (int e = 0; e < kAtOnce; ++e) {
-          if (j + e < run) {
-            v[e].load(x);
-            d[e].load(dy);
-          }
-          x += j + e < run ? hop : 0;
-          dy += j + e < run ? dhop : 0;
+      const int end = min(j0 + kRun, mine);
+#pragma unroll (BYTES >= 4 ? 1 : 4)
+      for (int j = j0; j < end; ++j) {
+        X v, d;
+        if constexpr (BYTES >= 4) {
+          fetch();
+          asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+          const unsigned char* const from = ring + (j % kAhead) * (2 * kThreads * BYTES);
+          v.load(reinterpret_cast<const T*>(from));
+          d.load(reinterpret_cast<const T*>(from + kThreads * BYTES));
+        } else {
+          v.load(x);
+          d.load(dy);
+          x += hop;
+          dy += dhop;
         }
+        P f[kPacks], g[kPacks];
+        v.open(f);
+        d.open(g);
 #pragma unroll
-        for (int e = 0; e < kAtOnce; ++e)
-          if (j + e < run) {
-            P f[kPacks], g[kPacks];
-            v[e].open(f);
-            d[e].open(g);
-#pragma unroll
-            for (int i = 0; i < kPacks; ++i) {
-              const P xhat = mul_(add_(f[i], q.mean[i * P::N / kStep]), q.rstd[i * P::N / kStep]);
-              const P dz = act_grad<T, ACT>(fma_(xhat, q.weight[i], q.bias[i]), g[i]);
-              s0[i] = add_(s0[i], dz);
-              s1[i] = fma_(dz, xhat, s1[i]);
-            }
-          }
+        for (int i = 0; i < kPacks; ++i) {
+          const P xhat = mul_(add_(f[i], q.mean[i * P::N / kStep]), q.rstd[i * P::N / kStep]);
+          const P dz = act_grad<T, ACT>(fma_(xhat, q.weight[i], q.bias[i]), g[i]);
+          s0[i] = add_(s0[i], dz);
+          s1[i] = fma_(dz, xhat, s1[i]);
+        }
       }
 #pragma unroll
       for (int i = 0; i < kPacks; ++i) total0[i] = add_(total0[i], s0[i]), total1[i] = add_(total1[i], s1[i]);
-      left -= run;
     }
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -861,7 +892,14 @@ template <class T, int BYTES, int Q, int ACT>
 int launch_blocks(bool backward, NormArgs& a, const Cut& k, cudaStream_t st) {
   const dim3 grid(k.col_blocks, k.row_blocks, a.B);
   if (backward) {
-    norm_sums_kernel<T, BYTES, Q, ACT><<<grid, kThreads, k.smem, st>>>(a);
+    static OncePerDevice once;
+    const auto sums = norm_sums_kernel<T, BYTES, Q, ACT>;
+    if (once.run(current_device(), [&] {
+          return int(cudaFuncSetAttribute(sums, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          kRingBytes<BYTES> + kThreads * 8 * BYTES / int(sizeof(T))));
+        }) != 0)
+      return TTT_ERR_CUDA;
+    sums<<<grid, kThreads, k.smem + kRingBytes<BYTES>, st>>>(a);
     launch_behind(norm_dx_kernel<T, BYTES, Q, ACT>, grid, kThreads, k.slots * 8, a, st);
     if (a.dweight || a.dbias) launch_behind(norm_dweight_kernel, dim3((a.C + 31) / 32), 1024, 0, a, st);
   } else {
