@@ -38,7 +38,8 @@ def nvcc_path() -> str:
 def _digest(path: str, flags: list[str]) -> str:
     h = hashlib.sha256()
     h.update(" ".join(flags).encode())
-    for f in sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [path]):
+    headers = [g for d, e in ((CSRC, "*.cuh"), (CSRC, "*.h"), (INCLUDE, "*.h")) for g in glob.glob(os.path.join(d, e))]
+    for f in sorted(headers + [path]):
         h.update(f.encode())
         with open(f, "rb") as fh:
             h.update(fh.read())
