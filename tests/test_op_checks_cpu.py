@@ -89,3 +89,18 @@ def test_columns_of_one_buffer_are_apart(lib):
         # the first tensor: columns 64..127 of 192; the second: 64 columns from column k on, those past
         # the last being the next token's first
         assert lib.s(1 << 20, 2, (64, n, s), (1 << 20) + 2 * (k - 64), (64, n, s)) == share, k
+
+
+@pytest.mark.parametrize("n,s,row", [((1, 3, 40), (0, 8, 96), 24),          # [B, N, 4 H d]: heads one behind the other
+                                     ((1, 40, 3), (7, 96, 8), 24),      # the same, dimensions in another order
+                                     ((2, 3, 20), (20 * 96, 8, 96), 24),    # batch entries one behind the other
+                                     ((4, 3, 5), (24, 8, 480), 96)])        # two dense dimensions
+def test_column_ranges_of_several_heads_are_apart(lib, n, s, row):
+    """The heads of one token lie densely in a wider row: what counts is the whole range of columns."""
+    at = 1 << 20
+    a = set(_places(at, 2, 8, n, s))
+    told = [lib.s(at, 2, (8, n, s), at + 2 * k, (8, n, s)) for k in range(-130, 131)]
+    assert told == [bool(a & set(_places(at + 2 * k, 2, 8, n, s))) for k in range(-130, 131)]
+    step = max(s)
+    for k, share in ((row, False), (row - 1, True), (step - row, False), (step - row + 1, True)):
+        assert lib.s(at, 2, (8, n, s), at + 2 * k, (8, n, s)) == share, k

@@ -708,6 +708,40 @@ def test_refusals_of_the_binding():
         ops.GroupNorm(dict(C=32, groups=5, dtype="f32"))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_column_ranges_of_a_fused_buffer_are_read_and_written(dtype):
+    """Several heads or groups: positions from one third of a fused projection into another, the norm from
+    one half of a buffer into the other, and their gradients the same way; what lies beside stays as it was."""
+    ops, gen, dt = _ops(), _gen(31), DT[dtype]
+    B, N, H, d = 2, 45, 3, 16
+    fused = torch.full((B, N, 3, H, d), 7.0, dtype=dt, device="cuda")
+    x = _randn(gen, B, H, N, d).to(dt)
+    fused[:, :, 0] = x.transpose(1, 2).cuda()
+    src, to = fused[:, :, 0].transpose(1, 2), fused[:, :, 2].transpose(1, 2)
+    pos = torch.arange(N, dtype=torch.int32)[:, None].contiguous()
+    rope = ops.RotaryPositions(dict(d=d, pairs=(6,), dtype=dtype))
+    for call in (rope.forward, rope.backward):
+        want = call(x.cuda(), pos.cuda())
+        assert call(src, pos.cuda(), out=to) is to and torch.equal(to, want)
+    assert torch.equal(src.cpu(), x) and (fused[:, :, 1] == 7.0).all()
+    C, G = 48, 4
+    norm = ops.GroupNorm(dict(C=C, groups=G, act="silu", dtype=dtype))
+    for rows in (N, 4000):  # one block a group, and two kernels
+        wide = torch.full((B, rows, 3 * C), 7.0, dtype=dt, device="cuda")
+        x, dy = (_randn(gen, B, rows, C).to(dt).cuda() for _ in range(2))
+        w, b = (_randn(gen, C).cuda() for _ in range(2))
+        wide[..., :C] = x
+        stats, again = norm.new_stats(B), norm.new_stats(B)
+        want = norm.forward(x, w, b, stats=stats)
+        assert torch.equal(norm.forward(wide[..., :C], w, b, stats=again, out=wide[..., 2 * C:]), want)
+        grads = norm.backward(dy, x, w, b, stats)
+        got = norm.backward(dy, wide[..., :C], w, b, again, dx=wide[..., 2 * C:])
+        assert all(torch.equal(p, q) for p, q in zip(grads, got))
+        assert torch.equal(wide[..., :C], x) and (wide[..., C:2 * C] == 7.0).all()
+        with pytest.raises(Exception, match="ttt_norm_forward"):  # one channel of the input
+            norm.forward(wide[..., :C], w, b, out=wide[..., C - 1:2 * C - 1])
+
+
 # --------------------------------------------------------------- the block together
 def test_positions_layer_norm_and_recurrence_as_one_block():
     """A token-mixing block as a model runs it: projections tokens first, rotary positions onto the layer's

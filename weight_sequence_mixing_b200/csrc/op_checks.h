@@ -73,27 +73,34 @@ inline bool same_tensor(const RowTensor& a, const RowTensor& b) {
 // Whether the tensors may share bytes.  Exact for tensors that do not interleave;
 // for two of the same shape and strides whose rows interleave (two column ranges of
 // one buffer), rows start at fixed remainders modulo the smallest stride, which
-// keeps them apart when the remainders do.  Anything else that interleaves counts
-// as sharing.
+// keeps them apart when the remainders do.  Dimensions that lie densely behind one
+// another (the heads of a token) count as one row.  Anything else that interleaves
+// counts as sharing.
 inline bool may_share(const RowTensor& a, const RowTensor& b) {
   if (a.empty() || b.empty()) return false;
   const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.ptr), b0 = reinterpret_cast<uintptr_t>(b.ptr);
   if (a0 + uintptr_t(a.span()) * a.elem <= b0 || b0 + uintptr_t(b.span()) * b.elem <= a0) return false;
   if (a.elem != b.elem || a.width != b.width) return true;
+  for (int i = 0; i < 3; ++i)
+    if (a.n[i] != b.n[i] || (a.n[i] > 1 && a.stride[i] != b.stride[i])) return true;
+  int64_t width = a.width;
+  bool folded[3] = {a.n[0] <= 1, a.n[1] <= 1, a.n[2] <= 1};
+  for (int pass = 0; pass < 3; ++pass)
+    for (int i = 0; i < 3; ++i)
+      if (!folded[i] && a.stride[i] == width) {
+        width *= a.n[i];  // at most the span
+        folded[i] = true;
+      }
   int64_t step = 0;
-  for (int i = 0; i < 3; ++i) {
-    if (a.n[i] != b.n[i]) return true;
-    if (a.n[i] <= 1) continue;
-    if (a.stride[i] != b.stride[i]) return true;
-    if (step == 0 || a.stride[i] < step) step = a.stride[i];
-  }
+  for (int i = 0; i < 3; ++i)
+    if (!folded[i] && (step == 0 || a.stride[i] < step)) step = a.stride[i];
   if (step == 0) return true;
   for (int i = 0; i < 3; ++i)
-    if (a.n[i] > 1 && a.stride[i] % step) return true;
+    if (!folded[i] && a.stride[i] % step) return true;
   const uint64_t gap = a0 < b0 ? b0 - a0 : a0 - b0;
   if (gap % a.elem) return true;
   const int64_t r = int64_t(gap / a.elem % uint64_t(step));
-  return r < a.width || step - r < a.width;
+  return r < width || step - r < width;
 }
 
 // whether every row of the tensor starts on a multiple of `bytes`
