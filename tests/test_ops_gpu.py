@@ -301,6 +301,37 @@ def test_scan_infinities_and_nan_stay_in_their_channel_and_batch_entry():
     assert torch.equal(h[1, :300, 5], clean["h"].cpu()[1, :300, 5])
 
 
+@pytest.mark.parametrize("L", [1, 16, 130, 600])
+@pytest.mark.parametrize("inp", ["plain", "complement"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_scan_sigmoid_gates_that_are_shut_or_open(dtype, inp, L):
+    """Gates about the borders of the exponential's range: e^-g is infinite from -88.7 on, 1 / (1 + e^-g)
+    below the normal range from -87.3 on (subnormal results are zero: 2^-126 off), e^-g so from 87.3 on."""
+    edges = (-math.inf, -200.0, -104.0, -89.0, -88.5, -88.0, -87.5, -87.0, -86.5, -42.0, -41.5, -30.0, 0.0, 15.0, 30.0,
+             87.0, 88.0, 89.0, 104.0, math.inf)
+    case = (2, L, len(edges) + 1, "sigmoid", inp, dtype, True, False, False)
+    d = _scan_inputs(case, 37)
+    at = torch.arange(L)
+    for c, e in enumerate(edges):  # a channel for each: at one token in three, at every one in the second entry
+        d["g"][0, at % 3 == c % 3, c] = e
+        d["g"][1, :, c] = e
+    got = _run_scan(case, d)
+    g, x, dh = d["g"].double(), d["x"].double(), d["dh"].double()
+    # infinite gates as finite ones that are as shut or open in 64 bits, so that no bound meets infinity times zero
+    want, err = ref.scan(g.clamp(-1e4, 1e4), x, "sigmoid", inp, d["h0"].double(), None, dh, d["dh_last"].double())
+    # a gate below the normal range counts as zero: 2^-126 of the state or the gradient that it scales
+    flush = 2.0 ** -126 * 8 * (1 + max(float(want[k].abs().max()) for k in want) ** 2)
+    # bf16 takes 2^y with y = -g log2 e rounded to 32 bits: y is off by |y| 2^-24, so e^-g by |g| log2(e) 2^-24 ln 2
+    # = |g| half steps, relative.  Every error that the reference counts has the gate's 12 half steps as its unit, of
+    # which this makes 12 + |g| (past 104, e^-|g| is below all of fp32)
+    more = torch.ones(len(edges) + 1, dtype=torch.float64)
+    if dtype == "bf16":
+        more[:-1] += torch.tensor([min(abs(e), 104.0) for e in edges]).double() * ref.E32 / ref.STEP
+    for k, v in want.items():
+        t = torch.float32 if k in ("h_last", "dh0") else DT[dtype]
+        ref.check(k, got[k], v, ref.rounded(v, err[k] * more, t) + flush)
+
+
 def test_scan_gradients_against_differences():
     """h is linear in x and in h0, and a polynomial in value gates: central differences of the fp32 kernel's
     <dh, h> + <dh_last, h_last> against its gradients, and the same step in 64 bits for the gates."""

@@ -130,8 +130,10 @@ __device__ __forceinline__ void gate(typename Word<T>::V g, typename Word<T>::V&
     if constexpr (GATE == TTT_GATE_SIGMOID) {
       const Two s = add_(e, W::all(1.f));
       a = two(rcp_fast(s[0]), rcp_fast(s[1]));
-      const Two q = mul_(e, a);  // infinity times zero where the gate is shut: the complement is one
-      rest = two(fminf(q[0], 1.f), fminf(q[1], 1.f));
+      // from 2^60 on the complement is one: e a would meet a reciprocal below the normal range (zero
+      // from 2^126 on), or an infinite e
+      const Two q = mul_(e, a);
+      rest = two(e[0] > 0x1p60f ? 1.f : fminf(q[0], 1.f), e[1] > 0x1p60f ? 1.f : fminf(q[1], 1.f));
     } else {
       a = e;
       // 1 - e^g: below 1/2 in size by the series of (1 - e^g) / -g, 2^-26 off at most, which
