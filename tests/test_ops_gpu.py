@@ -332,6 +332,29 @@ def test_scan_sigmoid_gates_that_are_shut_or_open(dtype, inp, L):
         ref.check(k, got[k], v, ref.rounded(v, err[k] * more, t) + flush)
 
 
+@pytest.mark.parametrize("L", [9, 300])
+@pytest.mark.parametrize("gate", ["value", "sigmoid", "exp"])
+@pytest.mark.parametrize("inp", ["plain", "complement"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_scan_nan_gates_give_nan_where_the_formula_does(dtype, inp, gate, L):
+    """A NaN gate at one token: that token's and later states, the gradients of that token's gate and input
+    (with the complement) and of earlier ones."""
+    case = (2, L, 6, gate, inp, dtype, True, False, False)
+    d = _scan_inputs(case, 41)
+    t = L // 2
+    d["g"][1, t, 3] = math.nan
+    got = {k: torch.isnan(v.cpu()) for k, v in _run_scan(case, d).items()}
+    at = torch.arange(L)
+    want = {k: torch.zeros_like(v) for k, v in got.items()}
+    want["h"][1, t:, 3] = want["h_last"][1, 3] = want["dh0"][1, 3] = True
+    want["dx"][1, :, 3] = (at <= t) if inp == "complement" else (at < t)
+    want["dg"][1, :, 3] = True  # lam before the token, h behind it, the slope at it (value: h_{t-1} lam there)
+    if gate == "value":
+        want["dg"][1, t, 3] = False
+    for k in want:
+        assert torch.equal(got[k], want[k]), (k, torch.nonzero(got[k] != want[k])[:4].tolist())
+
+
 def test_scan_gradients_against_differences():
     """h is linear in x and in h0, and a polynomial in value gates: central differences of the fp32 kernel's
     <dh, h> + <dh_last, h_last> against its gradients, and the same step in 64 bits for the gates."""

@@ -132,8 +132,8 @@ __device__ __forceinline__ void gate(typename Word<T>::V g, typename Word<T>::V&
       a = two(rcp_fast(s[0]), rcp_fast(s[1]));
       // from 2^60 on the complement is one: e a would meet a reciprocal below the normal range (zero
       // from 2^126 on), or an infinite e
-      const Two q = mul_(e, a);
-      rest = two(e[0] > 0x1p60f ? 1.f : fminf(q[0], 1.f), e[1] > 0x1p60f ? 1.f : fminf(q[1], 1.f));
+      const Two q = mul_(e, a);  // NaN where the gate is
+      rest = two(e[0] > 0x1p60f ? 1.f : q[0], e[1] > 0x1p60f ? 1.f : q[1]);
     } else {
       a = e;
       // 1 - e^g: below 1/2 in size by the series of (1 - e^g) / -g, 2^-26 off at most, which
