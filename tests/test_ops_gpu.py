@@ -267,6 +267,18 @@ def test_scan_of_no_tokens_hands_the_state_through():
     op.check_status()
 
 
+def test_scan_backward_of_no_tokens_reads_nothing_that_was_not_kept():
+    """Many more states than the smallest buffer holds (new_saved gives 16 bytes for no tokens)."""
+    B, D = 64, 4096
+    op = _ops().GatedScan(dict(D=D, gate="sigmoid", inp="complement", dtype="f32"))
+    e, dl = torch.empty((B, 0, D), device="cuda"), torch.randn(B, D, device="cuda")
+    saved = op.new_saved(B, 0)
+    assert saved.numel() == 16
+    dg, dx, dh0 = op.backward(e, e, e, saved, dh_last=dl)
+    op.check_status()
+    assert dg.shape == dx.shape == (B, 0, D) and torch.equal(dh0, dl)
+
+
 @pytest.mark.parametrize("dtype,D,parts", [("bf16", 72, (300, 1, 1, 517, 44)), ("f32", 33, (256, 257, 3))])
 def test_scan_in_parts_with_the_state_handed_on(dtype, D, parts):
     """The state written in the place of the one read, call after call, against one call over all tokens."""

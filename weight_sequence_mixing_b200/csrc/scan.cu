@@ -1100,7 +1100,7 @@ extern "C" int ttt_scan_backward(const ttt_scan* h, int32_t B, int64_t L, const 
   const int r = prepare(h, true, B, L, tiles, 3, out, 2, workspace, workspace_bytes, status, &a);
   if (r != TTT_OK) return r;
   a.dh = dh, a.g = g, a.x = x, a.dh_last = dh_last, a.lengths = lengths, a.dg = dg, a.dx = dx, a.dh0 = dh0;
-  a.saved = static_cast<float*>(const_cast<void*>(saved));
+  a.saved = nsaved ? static_cast<float*>(const_cast<void*>(saved)) : nullptr;  // no tokens: none kept, whatever is given
   put_strides(a.dhs, dhs), put_strides(a.gs, gs), put_strides(a.xs, xs), put_strides(a.dgs, dgs),
       put_strides(a.dxs, dxs);
   const int64_t strides[3][2] = {{gs->batch, gs->token}, {xs->batch, xs->token}, {dhs->batch, dhs->token}};
