@@ -616,6 +616,22 @@ def test_norm_of_a_group_far_from_zero(dtype, offset):
         ref.check(k, v, want[k], ref.rounded(want[k], err[k], DT[dtype] if k == "y" else torch.float32))
 
 
+@pytest.mark.parametrize("case", [(2, 100, 96, 32, "gelu", "f32", "tokens"), (2, 4100, 96, 6, "silu", "bf16", "tokens")],
+                         ids=["one_block_a_group", "two_kernels"])
+def test_norm_small_tensors_at_any_place_of_a_buffer(case):
+    """Statistics, weights and their gradients one fp32 value past the alignment of a buffer."""
+    B, N, C, G, act, dtype, layout = case
+    x, xd, w, b, dy = _norm_inputs(case)
+    op = _ops().GroupNorm(dict(C=C, groups=G, act=act, dtype=dtype))
+    odd = lambda *shape: torch.empty(1 + math.prod(shape), device="cuda")[1:].view(shape)  # noqa: E731
+    stats = op.new_stats(B)
+    want = [op.forward(xd, w.cuda(), b.cuda(), stats=stats), *op.backward(dy.cuda(), xd, w.cuda(), b.cuda(), stats)]
+    wd, bd, st, dw, db = odd(C).copy_(w), odd(C).copy_(b), odd(B, G, 2), odd(C), odd(C)
+    assert all(t.data_ptr() % 8 == 4 for t in (wd, bd, st, dw, db))
+    got = [op.forward(xd, wd, bd, stats=st), *op.backward(dy.cuda(), xd, wd, bd, st, dweight=dw, dbias=db)]
+    assert torch.equal(st, stats) and all(torch.equal(p, q) for p, q in zip(want, got))
+
+
 def test_norm_nan_stays_in_its_group_and_batch_entry():
     case = (3, 150, 64, 4, "silu", "bf16", "tokens")
     x, xd, w, b, dy = _norm_inputs(case)

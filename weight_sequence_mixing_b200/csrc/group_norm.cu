@@ -53,6 +53,10 @@ struct NormArgs {
   int32_t slots;                         // groups of a block of channels at most
 };
 
+// Group k's (mean, 1 / sqrt(var + eps)), each on its own: the caller's buffer is aligned to its elements only
+__device__ __forceinline__ float2 load_stats(const float* stats, int64_t k) { return make_float2(stats[2 * k], stats[2 * k + 1]); }
+__device__ __forceinline__ void store_stats(float* stats, int64_t k, float2 m) { stats[2 * k] = m.x, stats[2 * k + 1] = m.y; }
+
 struct Part {  // of n values: their mean, and S the sum of squares about it
   float n, mean, S;
 };
@@ -317,8 +321,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_apply_kernel(const __grid_co
                             p.eps);
     if (threadIdx.x % 32 == 0) {
       known[g - g0] = m;
-      if (p.stats && rb == 0 && g * p.n >= c0)
-        reinterpret_cast<float2*>(p.stats)[int64_t(b) * p.G + g] = m;
+      if (p.stats && rb == 0 && g * p.n >= c0) store_stats(p.stats, int64_t(b) * p.G + g, m);
     }
   }
   __syncthreads();
@@ -388,7 +391,7 @@ struct Known {
 #pragma unroll
       for (int e = 0; e < P::N; ++e) {
         const int k = c + i * P::N + e;
-        const float2 s = reinterpret_cast<const float2*>(p.stats)[int64_t(b) * p.G + k / p.n];
+        const float2 s = load_stats(p.stats, int64_t(b) * p.G + k / p.n);
         m[e] = -s.x;
         r[e] = s.y;
         w[e] = p.weight ? p.weight[k] : 1.f;
@@ -698,7 +701,7 @@ __global__ void __launch_bounds__(kSmallThreads) norm_small_kernel(const __grid_
   // what the mean's rounding left over, taken off the variance and added to the mean
   const float off = s.y / count, centre = mean + off;
   const float rstd = 1.f / sqrtf(fmaxf(s.x / count - off * off, 0.f) + p.eps);
-  if (p.stats && threadIdx.x == 0) reinterpret_cast<float2*>(p.stats)[int64_t(b) * p.G + g] = make_float2(centre, rstd);
+  if (p.stats && threadIdx.x == 0) store_stats(p.stats, int64_t(b) * p.G + g, make_float2(centre, rstd));
   for (int i = lane * V; i < p.n; i += p.lanes * V) {
     float scale[V], shift[V];
 #pragma unroll
@@ -735,7 +738,7 @@ __global__ void __launch_bounds__(kSmallThreads) norm_small_grad_kernel(const __
   T* dx = static_cast<T*>(p.dx) + b * p.dxs[0] + g * p.dxs[1];
   float* const dzs = values + int(p.N) * p.n;
   float2* const sums = reinterpret_cast<float2*>(dzs + int(p.N) * p.n);
-  const float2 m = reinterpret_cast<const float2*>(p.stats)[int64_t(b) * p.G + g];
+  const float2 m = load_stats(p.stats, int64_t(b) * p.G + g);
   float2 q = make_float2(0.f, 0.f);
   if (here)
     for (int i = lane * V; i < p.n; i += p.lanes * V) {
