@@ -513,6 +513,24 @@ def test_scan_longer_than_32_bit_offsets():
     assert (h[0, -501] == 101.0).all() and (h[0, -700:-600] == 1.0).all()
 
 
+def test_scan_clear_of_as_many_sequences_as_there_can_be():
+    """2^31 - 1 sequences of one token and channel, one in a million of them with a token of its own."""
+    from weight_sequence_mixing_b200.binding import LIB
+    import ctypes
+    B = 2 ** 31 - 1
+    op = _ops().GatedScan(dict(D=1, gate="value", inp="plain", dtype="bf16"))
+    y = torch.ones(B, dtype=torch.bfloat16, device="cuda")
+    n = torch.zeros(B, dtype=torch.int32, device="cuda")
+    n[::1_000_003] = 1
+    n[-1] = 1
+    status = LIB.ttt_scan_clear(op._handle, B, 1, n.data_ptr(), y.data_ptr(), (ctypes.c_int64 * 3)(1, 0, 1),
+                                torch.cuda.current_stream().cuda_stream)
+    assert status == 0
+    torch.cuda.synchronize()
+    assert (y[::1_000_003] == 1).all() and y[-1] == 1
+    assert sum(int(torch.count_nonzero(part)) for part in y.split(1 << 28)) == len(range(0, B, 1_000_003)) + 1
+
+
 # ------------------------------------------------------------------------- norm
 # B, N, C, G, act, dtype, layout ("tokens": [B,N,C]; "heads": [B,G,N,C/G]; "slice"; "odd")
 NORM = [

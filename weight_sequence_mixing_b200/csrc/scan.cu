@@ -870,7 +870,8 @@ __global__ void __launch_bounds__(128) scan_short_kernel(const __grid_constant__
 template <class T>
 __global__ void __launch_bounds__(256) scan_clear_kernel(const int* lengths, T* y, int64_t sb, int64_t st, int64_t L, int B, int D) {
   const int per = gridDim.x / B, lane = threadIdx.x % 32;  // blocks of a sequence; fewer than one: sequences of a block
-  for (int b = per ? blockIdx.x / per : blockIdx.x; b < B; b += per ? B : gridDim.x) {
+  // 64 bits: the last step of up to 2^31 - 1 sequences goes beyond them
+  for (int64_t b = per ? blockIdx.x / per : blockIdx.x; b < B; b += per ? B : gridDim.x) {
     const int first = per ? blockIdx.x % per : 0, hop = per ? per : 1;
     if (first >= hop) break;
     for (int64_t t = max(lengths[b], 0) + int64_t(first) * 8 + threadIdx.x / 32; t < L; t += int64_t(hop) * 8)
