@@ -9,6 +9,7 @@
 #define TTT_DIAG_H_
 
 #include "ttt.h"
+#include "ttt_ops.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -56,6 +57,15 @@ int ttt_plan_info(const ttt_handle* handle, int* info, int n);
  * TTT_ERR_TIMEOUT when the wait ran out (the expected result), TTT_OK otherwise,
  * TTT_ERR_CUDA / TTT_ERR_INVALID_ARG on a launch or argument error. */
 int ttt_selftest_timeout(void* status_word, void* stream);
+
+/* The same inside the gated recurrence: ttt_scan_forward over sequences of several tiles of which
+ * the first is never handed out, so that every tile behind it waits for its state in vain.  Waits
+ * give up after `wait_ms` (1 to 2000), the status gets bit 1, and every block ends with no copy in
+ * flight; h is not to be used.  `status` is required.  Enqueued on `stream`; TTT_ERR_UNSUPPORTED for
+ * sequences of one tile, which wait for nothing. */
+int ttt_selftest_scan_timeout(const ttt_scan* handle, int32_t B, int64_t L, const void* g, const ttt_strides* gs,
+                              const void* x, const ttt_strides* xs, void* h, const ttt_strides* hs, void* workspace,
+                              size_t workspace_bytes, unsigned* status, int32_t wait_ms, void* stream);
 
 /* Per-stage timing of a handle's forward calls.  ttt_profile_enable(h, 1)
  * clears earlier records and starts recording a CUDA event pair around every

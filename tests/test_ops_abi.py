@@ -238,3 +238,17 @@ def test_the_binding_refuses_what_is_not_on_its_device():
         ops.RotaryPositions(dict(d=8, pairs=(4,), dtype="f16"))
     with pytest.raises(ValueError):
         ops.RotaryPositions(dict(d=8, pairs=(4,), dtype="bf16"), device="cpu")
+
+
+def test_scan_timeout_selftest_calls_that_are_refused():
+    binding, ops = _lib()
+    st, h = _open("scan", ops.ScanConfig(D=64, gate=1, input=1, dtype=1))
+    call = lambda h=h, L=700, status=99 * M, ms=20, ws=160 * M: binding.LIB.ttt_selftest_scan_timeout(  # noqa: E731
+        h, 2, L, 64 * M, _s(L * 64, 0, 64), 80 * M, _s(L * 64, 0, 64), 112 * M, _s(L * 64, 0, 64), ws, 1 << 30, status, ms,
+        None)
+    for bad in (dict(h=None), dict(status=None), dict(ms=0), dict(ms=2001), dict(ms=-1), dict(ws=160 * M + 8)):
+        assert call(**bad) == binding.TTT_ERR_INVALID_ARG, bad
+    assert call(ws=None) == binding.TTT_ERR_WORKSPACE
+    for L in (0, 1, 16, 17, 256):  # no tile waits for another
+        assert call(L=L) == binding.TTT_ERR_UNSUPPORTED, L
+    binding.LIB.ttt_scan_destroy(h)

@@ -531,6 +531,41 @@ def test_scan_clear_of_as_many_sequences_as_there_can_be():
     assert sum(int(torch.count_nonzero(part)) for part in y.split(1 << 28)) == len(range(0, B, 1_000_003)) + 1
 
 
+@pytest.mark.parametrize("dtype,D,wide", [("bf16", 128, 128), ("bf16", 128, 130), ("bf16", 65, 65), ("f32", 33, 33)],
+                         ids=["tma", "copies_of_4", "odd_rows", "fp32_copies"])
+def test_scan_wait_that_runs_out_sets_the_status_and_ends(dtype, D, wide):
+    """The first tile is left out: what waits for its state gives up, in every form of the loads, and the
+    next call on the same buffers is right."""
+    import ctypes
+    from weight_sequence_mixing_b200.binding import LIB, TTT_ERR_TIMEOUT, TTTError
+    case = (3, 9 * 256 + 40, D, "sigmoid", "complement", dtype, False, False, False)
+    d = _scan_inputs(case)
+    B, L = case[:2]
+    rows = [torch.zeros((B, L, wide), dtype=DT[dtype], device="cuda") for _ in range(3)]
+    g, x, h = (t[..., :D] for t in rows)
+    g.copy_(d["g"]), x.copy_(d["x"])
+    op = _ops().GatedScan(dict(D=D, gate="sigmoid", inp="complement", dtype=dtype))
+    need = LIB.ttt_scan_workspace_size(op._handle, B, L)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    s = (ctypes.c_int64 * 3)(L * wide, 0, wide)
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    begin.record()
+    st = LIB.ttt_selftest_scan_timeout(op._handle, B, L, g.data_ptr(), s, x.data_ptr(), s, h.data_ptr(), s, ws.data_ptr(),
+                                       need, op._status.data_ptr(), 20, torch.cuda.current_stream().cuda_stream)
+    end.record()
+    assert st == 0
+    with pytest.raises(TTTError) as e:
+        op.check_status()
+    assert e.value.status == TTT_ERR_TIMEOUT
+    assert 20 <= begin.elapsed_time(end) < 2000
+    op.check_status()  # told once
+    got, last = op.forward(g, x, out=h)
+    op.check_status()
+    want, err = ref.scan(d["g"].double(), d["x"].double(), "sigmoid", "complement")
+    ref.check("h", got, want["h"], ref.rounded(want["h"], err["h"], DT[dtype]))
+    ref.check("h_last", last, want["h_last"], ref.rounded(want["h_last"], err["h_last"], torch.float32))
+
+
 # ------------------------------------------------------------------------- norm
 # B, N, C, G, act, dtype, layout ("tokens": [B,N,C]; "heads": [B,G,N,C/G]; "slice"; "odd")
 NORM = [

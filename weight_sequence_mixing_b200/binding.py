@@ -42,7 +42,7 @@ EXPORTED = [
     "ttt_state_size", "ttt_forward_state", "ttt_selftest_activation", "ttt_pair_schedule",
     "ttt_rope_create", "ttt_rope_destroy", "ttt_rope_apply",
     "ttt_scan_create", "ttt_scan_destroy", "ttt_scan_workspace_size", "ttt_scan_saved_size", "ttt_scan_forward",
-    "ttt_scan_backward", "ttt_scan_clear",
+    "ttt_scan_backward", "ttt_scan_clear", "ttt_selftest_scan_timeout",
     "ttt_norm_create", "ttt_norm_destroy", "ttt_norm_workspace_size", "ttt_norm_forward", "ttt_norm_backward",
 ]
 NUM_STAGES = 8
@@ -108,6 +108,7 @@ def _load():
         "ttt_scan_backward": (i32, [vp, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp,
                                     vp]),
         "ttt_scan_clear": (i32, [vp, i32, i64, vp, vp, vp, vp]),
+        "ttt_selftest_scan_timeout": (i32, [vp, i32, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp, i32, vp]),
         "ttt_norm_create": (i32, [vp, ctypes.POINTER(vp)]),
         "ttt_norm_destroy": (None, [vp]),
         "ttt_norm_workspace_size": (sz, [vp, i32, i64, i32]),

@@ -46,6 +46,7 @@
 #include <algorithm>
 #include <new>
 
+#include "../../include/ttt_diag.h"
 #include "op_checks.h"
 #include "per_device.h"
 #include "ptx.cuh"
@@ -85,6 +86,7 @@ struct ScanArgs {
   int32_t load;           // kLoadTma, kLoad4, kLoad2
   int32_t wide;           // outputs take 4-byte stores
   int32_t kept;           // kept states of a sequence
+  unsigned long long wait_ns;  // the longest wait
 };
 
 // The values of a lane's 4 bytes: one fp32 or two bf16.
@@ -298,7 +300,7 @@ __device__ __forceinline__ void look_back(const ScanArgs& p, int t, int before, 
     if (spin % 64 == 63) {
       const unsigned long long now = __shfl_sync(~0u, global_ns(), 0);
       if (!since) since = now;
-      if (now - since > kWaitLimitNs) break;
+      if (now - since > p.wait_ns) break;
     }
   }
   if (threadIdx.x % 32 == 0 && p.status) atomicOr(p.status, kStatusTimeout);
@@ -454,9 +456,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // Every wait is bounded; one that runs out ends the block's work with the status set.
   auto wait = [&](uint64_t* bar, int turn) {
-    const bool ok = mbar_wait(bar, turn & 1, &sc.abort);
+    const bool ok = mbar_wait(bar, turn & 1, &sc.abort, p.wait_ns);
     if (!ok && p.status && lane == 0) atomicOr(p.status, kStatusTimeout);
     return __all_sync(~0u, ok) != 0;
+  };
+  // the same in a warp that fetches rows itself: its copies in flight end before it does
+  auto wait_or_end = [&](uint64_t* bar, int turn) {
+    const bool ok = wait(bar, turn);
+    if (!TMA && !ok) asm volatile("cp.async.wait_all;" ::: "memory");
+    return ok;
   };
 
   if (warp == kFeedWarp) {
@@ -520,11 +528,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++k;
     }
-    // copies in flight end before the block does: after a wait that ran out, nobody else waits for them
-    if (*(volatile int*)&sc.abort) {
-      int given_up = 0;
-      for (int m = k > kJobs ? k - kJobs : 0; m < k; ++m) mbar_wait(&sc.full[m % kJobs], m / kJobs & 1, &given_up);
-    }
+    // copies in flight end before the block does: where a wait runs out, nobody else waits for them
+    int given_up = 0;
+    for (int m = k > kJobs ? k - kJobs : 0; m < k; ++m) mbar_wait(&sc.full[m % kJobs], m / kJobs & 1, &given_up, p.wait_ns);
     return;
   }
 
@@ -626,10 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto fetch_own = [&] {
     if (more) {
       const int s = fetched % kStages;
-      if (!wait(&sc.full[fetched % kJobs], fetched / kJobs)) {
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        return false;
-      }
+      if (!wait_or_end(&sc.full[fetched % kJobs], fetched / kJobs)) return false;
       const Job job = sc.job[fetched % kJobs];
       more = job.t >= 0;
       if (more) {
@@ -698,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (k < 0 || cur.t >= 0) {
       const int par = (k + 1) & 1;
       if (!TMA && !fetch_own()) return;  // tile k + kStages - 1
-      if (!wait(&sc.full[ahead.job], ahead.round)) return;
+      if (!wait_or_end(&sc.full[ahead.job], ahead.round)) return;
       if (!TMA) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");  // tile k + 1 is there
         __syncwarp();
@@ -741,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = left >= kRows && (cur.col + 1) * 32 * N <= p.D && (N == 1 || p.wide);
       const Rows rows = rows_of(here.stage, cur);
       auto word = [&](int tensor, int r) { return word_of(rows, tensor, r); };
-      if (!wait(&sc.entered[par], k >> 1)) return;
+      if (!wait_or_end(&sc.entered[par], k >> 1)) return;
       V st = sc.H[par][warp][lane];
       if constexpr (!BACKWARD) {
         T* to = static_cast<T*>(p.h) + cur.out[0] + mine0;
@@ -891,8 +894,9 @@ Space space_of(int64_t tiles, int per_word) {
   return s;
 }
 
+// `stuck`: the first tile is never handed out, so that all that waits for its state waits in vain
 template <class T, int GATE, int INPUT, bool BACKWARD>
-int launch(ScanArgs& a, const int64_t (*strides)[2], cudaStream_t st) {
+int launch(ScanArgs& a, const int64_t (*strides)[2], bool stuck, cudaStream_t st) {
   using S = Shape<T, BACKWARD>;
   if (a.L <= kShort) {
     const int64_t n = int64_t(a.B) * ((a.D + S::N - 1) / S::N), grid = (n + 127) / 128;
@@ -919,11 +923,12 @@ int launch(ScanArgs& a, const int64_t (*strides)[2], cudaStream_t st) {
   // all ones: nothing published, and a counter whose first answer is -1
   if (a.counter && cudaMemsetAsync(a.counter, 0xff, space_of(a.total, S::N).total, st) != cudaSuccess)
     return TTT_ERR_CUDA;
+  if (stuck && cudaMemsetAsync(a.counter, 0, sizeof(unsigned), st) != cudaSuccess) return TTT_ERR_CUDA;
   kernel<<<grid, kThreads, S::kSmem, st>>>(a, m[0], m[1], m[2]);
   return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
 }
 
-using Launch = int (*)(ScanArgs&, const int64_t (*)[2], cudaStream_t);
+using Launch = int (*)(ScanArgs&, const int64_t (*)[2], bool, cudaStream_t);
 template <class T, bool BACKWARD>
 Launch pick(int gate, int input) {
   constexpr int P = TTT_SCAN_PLAIN, C = TTT_SCAN_COMPLEMENT;
@@ -1028,6 +1033,7 @@ int prepare(const ttt_scan* h, bool backward, int32_t B, int64_t L, const RowTen
   const size_t need = ttt_scan_workspace_size(h, B, L);
   if (need && (!workspace || workspace_bytes < need)) return TTT_ERR_WORKSPACE;
   a->L = L, a->B = B, a->D = h->cfg.D;
+  a->wait_ns = kWaitLimitNs;
   a->status = status;
   a->per_col = int32_t(up(L, tile_tokens(backward)));
   a->kept = int32_t(up(L, kSave));
@@ -1057,10 +1063,12 @@ int prepare(const ttt_scan* h, bool backward, int32_t B, int64_t L, const RowTen
 
 }  // namespace
 
-extern "C" int ttt_scan_forward(const ttt_scan* h, int32_t B, int64_t L, const void* g, const ttt_strides* gs,
-                                const void* x, const ttt_strides* xs, const float* h0, const int32_t* lengths, void* ho,
-                                const ttt_strides* hs, float* h_last, void* saved, void* workspace,
-                                size_t workspace_bytes, unsigned* status, void* stream) {
+namespace {
+
+// ttt_scan_forward; with `stuck_ns`, its first tile is left out and waits are that long at most
+int forward(const ttt_scan* h, int32_t B, int64_t L, const void* g, const ttt_strides* gs, const void* x, const ttt_strides* xs,
+            const float* h0, const int32_t* lengths, void* ho, const ttt_strides* hs, float* h_last, void* saved,
+            void* workspace, size_t workspace_bytes, unsigned* status, unsigned long long stuck_ns, void* stream) {
   if (!scan_sizes_ok(h, B, L) || !gs || !xs || !hs) return TTT_ERR_INVALID_ARG;
   if (L > kMaxTokens) return TTT_ERR_UNSUPPORTED;
   if (!is_aligned(saved, 16) || !is_aligned(workspace, 16) || !is_aligned(status, 4)) return TTT_ERR_INVALID_ARG;
@@ -1076,10 +1084,32 @@ extern "C" int ttt_scan_forward(const ttt_scan* h, int32_t B, int64_t L, const v
   a.g = g, a.x = x, a.h0 = h0, a.lengths = lengths, a.h = ho, a.h_last = h_last;
   a.saved = static_cast<float*>(saved);
   put_strides(a.gs, gs), put_strides(a.xs, xs), put_strides(a.hs, hs);
+  if (stuck_ns) {
+    if (!a.counter) return TTT_ERR_UNSUPPORTED;  // sequences of one tile wait for nothing
+    a.wait_ns = stuck_ns;
+  }
   const int64_t strides[2][2] = {{gs->batch, gs->token}, {xs->batch, xs->token}};
   const Launch f = h->cfg.dtype == TTT_BF16 ? pick<__nv_bfloat16, false>(h->cfg.gate, h->cfg.input)
                                             : pick<float, false>(h->cfg.gate, h->cfg.input);
-  return f(a, strides, static_cast<cudaStream_t>(stream));
+  return f(a, strides, stuck_ns != 0, static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+extern "C" int ttt_scan_forward(const ttt_scan* h, int32_t B, int64_t L, const void* g, const ttt_strides* gs,
+                                const void* x, const ttt_strides* xs, const float* h0, const int32_t* lengths, void* ho,
+                                const ttt_strides* hs, float* h_last, void* saved, void* workspace,
+                                size_t workspace_bytes, unsigned* status, void* stream) {
+  return forward(h, B, L, g, gs, x, xs, h0, lengths, ho, hs, h_last, saved, workspace, workspace_bytes, status, 0, stream);
+}
+
+extern "C" int ttt_selftest_scan_timeout(const ttt_scan* h, int32_t B, int64_t L, const void* g, const ttt_strides* gs,
+                                         const void* x, const ttt_strides* xs, void* ho, const ttt_strides* hs,
+                                         void* workspace, size_t workspace_bytes, unsigned* status, int32_t wait_ms,
+                                         void* stream) {
+  if (!status || wait_ms < 1 || wait_ms > 2000) return TTT_ERR_INVALID_ARG;
+  return forward(h, B, L, g, gs, x, xs, nullptr, nullptr, ho, hs, nullptr, nullptr, workspace, workspace_bytes, status,
+                 wait_ms * 1000000ull, stream);
 }
 
 extern "C" int ttt_scan_backward(const ttt_scan* h, int32_t B, int64_t L, const void* dh, const ttt_strides* dhs,
@@ -1107,7 +1137,7 @@ extern "C" int ttt_scan_backward(const ttt_scan* h, int32_t B, int64_t L, const 
   const int64_t strides[3][2] = {{gs->batch, gs->token}, {xs->batch, xs->token}, {dhs->batch, dhs->token}};
   const Launch f = h->cfg.dtype == TTT_BF16 ? pick<__nv_bfloat16, true>(h->cfg.gate, h->cfg.input)
                                             : pick<float, true>(h->cfg.gate, h->cfg.input);
-  return f(a, strides, static_cast<cudaStream_t>(stream));
+  return f(a, strides, false, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int ttt_scan_clear(const ttt_scan* h, int32_t B, int64_t L, const int32_t* lengths, void* y,
