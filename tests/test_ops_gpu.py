@@ -685,6 +685,32 @@ def test_norm_small_tensors_at_any_place_of_a_buffer(case):
     assert torch.equal(st, stats) and all(torch.equal(p, q) for p, q in zip(want, got))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G,N", [(64, 20), (1, 40)], ids=["one_block_a_group", "two_kernels"])
+def test_norm_gelu_keeps_its_digits_in_the_tail(dtype, G, N):
+    """With a weight of zero z is the bias itself: z Phi(z) and, through dbias of a single dy, its slope, from
+    -13 (where they are next to the least normal number) on, relative to the values."""
+    C = 1024
+    z = torch.linspace(-13.0, 9.0, C)
+    op = _ops().GroupNorm(dict(C=C, groups=G, act="gelu", dtype=dtype))
+    x = _randn(_gen(8), 1, N, C).to(DT[dtype]).cuda()
+    w, b, stats = torch.zeros(C, device="cuda"), z.cuda(), op.new_stats(1)
+    y = op.forward(x, w, b, stats=stats)
+    dy = torch.zeros((1, N, C), dtype=DT[dtype], device="cuda")
+    dy[0, N // 2] = 1.0
+    _, _, slope = op.backward(dy, x, w, b, stats)
+    z = z.double()
+    cdf, pdf = 0.5 * torch.erfc(-z / math.sqrt(2)), torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    # the exponent z^2 log2(e) / 2 <= 122 is rounded twice, its constant once: 1.5 2^-23 of it at most, times ln 2
+    # 1.5e-5 in its exponential (erfc's argument, squared, is the same); the exponential itself, a reciprocal and the
+    # polynomial 1.2e-6 more: in all below 2^-15
+    off = 2.0 ** -15
+    want = (z * cdf).expand(1, N, C)
+    ref.check("y", y, want, ref.rounded(want, off * want.abs(), DT[dtype]))
+    want = cdf + z * pdf
+    ref.check("slope", slope, want, ref.rounded(want, off * (cdf + z.abs() * pdf), torch.float32))
+
+
 def test_norm_nan_stays_in_its_group_and_batch_entry():
     case = (3, 150, 64, 4, "silu", "bf16", "tokens")
     x, xd, w, b, dy = _norm_inputs(case)
