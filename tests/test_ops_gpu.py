@@ -109,6 +109,28 @@ def test_rope_backward_is_the_gradient_of_forward():
     assert abs(got - want) <= size
 
 
+@pytest.mark.parametrize("kind", [torch.int32, torch.float32])
+def test_rope_fp32_keeps_the_digits_of_small_sines(kind):
+    """Angles next to every quarter of a turn, of which only the fp32 value of the rest is rounded: p radians for
+    the integers p nearest to multiples of pi / 2, and turns of far positions."""
+    near = [0, 1, 3, 11, 22, 33, 44, 344, 355, 366, 377, 710, 51819, 52174, 103993, 104348, 208341, 312689, 833719, 1146408,
+            4272943, 5419351]
+    near = [p * s for p in near for s in (1, -1)]
+    pos = torch.tensor(near, dtype=torch.float64).to(kind)[:, None].contiguous()
+    x = torch.zeros(1, 1, len(near), 4)
+    x[..., 0] = 1.0  # its pair's cosine and sine
+    op = _ops().RotaryPositions(dict(d=4, pairs=(2,), base=10000.0, dtype="f32"))
+    y = op.forward(x.cuda(), pos.cuda()).cpu()[0, 0].double()
+    cos, sin = torch.cos(pos[:, 0].double()), torch.sin(pos[:, 0].double())
+    # integers: the frequency is exact to 2^-64 turns, so the angle to |p| 2^-61.3 radians; fp32 positions: it is
+    # rounded to 64 bits and so is their product, each 2^-53 of the angle (p radians) at most.  Then relative: the rest's rounding 2^-24, the sine's polynomial 3e-9, its
+    # small terms a tenth of a half step and its last sum one; the cosine's last sum one, and three tenths of one
+    # before it.  Below 2.5 half steps, and one for the product with 1 and the sum with 0.
+    off = pos[:, 0].double().abs() * (2.0 ** -61.3 if kind == torch.int32 else 2.0 ** -52)
+    ref.check("cos", y[:, 0], cos, off + 3.5 * ref.E32 * cos.abs())
+    ref.check("sin", y[:, 2], sin, off + 3.5 * ref.E32 * sin.abs())
+
+
 def test_rope_rows_beyond_32_bit_offsets():
     """The last rows of a tensor of more than 2^31 elements, read and written at 64-bit offsets."""
     N, d = (1 << 25) + 3, 72
