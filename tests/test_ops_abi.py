@@ -252,3 +252,12 @@ def test_scan_timeout_selftest_calls_that_are_refused():
     for L in (0, 1, 16, 17, 256):  # no tile waits for another
         assert call(L=L) == binding.TTT_ERR_UNSUPPORTED, L
     binding.LIB.ttt_scan_destroy(h)
+
+
+@pytest.mark.parametrize("L,states", [(0, 0), (1, 1), (16, 1), (128, 1), (129, 2), (256, 2), (257, 3), (5001, 40)])
+def test_scan_keeps_the_states_that_backward_reads(L, states):
+    """One for each of the backward pass's tiles of 128 tokens, fp32."""
+    binding, ops = _lib()
+    st, h = _open("scan", ops.ScanConfig(D=33, gate=1, input=1, dtype=1))
+    assert st == 0 and binding.LIB.ttt_scan_saved_size(h, 5, L) == 5 * states * 33 * 4
+    binding.LIB.ttt_scan_destroy(h)

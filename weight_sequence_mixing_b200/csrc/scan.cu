@@ -32,7 +32,7 @@
 //     one, so a result has the same bits whichever tile's state was found first.
 // The backward pass is the same over the tokens last to first; the states h_{t-1} that the
 // gates' gradient needs are formed again in fp32 from states that the forward pass kept
-// (one in 64 tokens), not read back rounded.
+// (one in 128 tokens, a backward tile), not read back rounded.
 //
 // Measured, bf16, 1024 channels: forward over 1029120 tokens 1.26 ms (77% of the copy
 // bandwidth; exponential gate), over 64 sequences of 2048 140 us (88%; plain gate), 181 us
@@ -62,7 +62,7 @@ constexpr int kChainWarp = kWarps;     // two warps that follow the chain of sta
 constexpr int kFeedWarp = kWarps + 2;  // the warp that hands out tiles and fetches their rows
 constexpr int kThreads = 32 * (kWarps + 3);
 constexpr int kRowBytes = 128;     // a tile's channels: 32 lanes of 4 bytes
-constexpr int kSave = 64;          // tokens from one kept state to the next
+constexpr int kSave = 128;         // tokens from one kept state to the next: a backward tile
 constexpr int kShort = 16;         // longest sequence of the short form
 constexpr int kWindow = 64;        // earlier tiles looked at
 enum : int { kLoadTma = 0, kLoad4 = 1, kLoad2 = 2 };
@@ -358,6 +358,7 @@ struct Shape {
   static constexpr int N = Word<T>::N;
   static constexpr int kRows = BACKWARD ? 8 : 16;  // tokens of a warp
   static constexpr int kTile = kWarps * kRows;
+  static_assert(BACKWARD ? kTile == kSave : kTile % kSave == 0, "each backward tile starts from a kept state, and no other is kept");
   static constexpr int kBox = kTile * kRowBytes;  // bytes of one tensor's tile
   static constexpr int kTensors = BACKWARD ? 3 : 2;
   static constexpr int kStages = BACKWARD ? 4 : 3;
