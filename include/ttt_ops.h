@@ -28,7 +28,9 @@
  *   - `status` (optional, 4 bytes of device memory) collects the device status bits:
  *     a call that goes wrong on the device sets bits, and its outputs are then not to
  *     be used; no call clears them.  Bit 1 (value 2): a bounded device wait ran out
- *     (2 s, as in ttt.h).
+ *     (2 s, as in ttt.h).  Only the recurrence waits on other blocks: rotary positions
+ *     take no status, and the norm takes one, as all calls with a workspace do, and
+ *     never sets it.
  *   - Results do not depend on timing: the same call gives the same bits.  Rows that
  *     start on other alignments or strides may take another kernel, of the same
  *     definition and arithmetic, whose last bits may differ.
@@ -54,14 +56,17 @@ typedef struct ttt_strides {
  * the pair over all axes and M = sum of pairs:
  *   y[p] = x[p] cos phi - x[q] sin phi,   y[q] = x[q] cos phi + x[p] sin phi,
  *   (p, q) = (i, i + M) with TTT_ROPE_HALVES, (2i, 2i + 1) with TTT_ROPE_INTERLEAVED.
- * Channels from 2M on are copied.  Angles are formed and reduced in 64 bits. */
+ * Channels from 2M on are copied.  Angles are formed and reduced in 64 bits.  Before
+ * its rounding to `dtype` an output is off by 2^-22 (|x[p]| + |x[q]|) at most in fp32, by
+ * 2^-20 of them in bf16.
+ * TTT_ERR_UNSUPPORTED: d above 4096, more than TTT_ROPE_MAX_PAIRS pairs, N above 2^40. */
 typedef enum { TTT_ROPE_HALVES = 0, TTT_ROPE_INTERLEAVED = 1 } ttt_rope_pairing;
 typedef enum { TTT_POS_I32 = 0, TTT_POS_F32 = 1 } ttt_pos_dtype;
 #define TTT_ROPE_MAX_AXES 4
 #define TTT_ROPE_MAX_PAIRS 256
 
 typedef struct ttt_rope_config {
-  int32_t d;                        /* channels of a head, >= 2 * sum(pairs) */
+  int32_t d;                        /* channels of a head, >= 2 * sum(pairs), at most 4096 */
   int32_t axes;                     /* 1..TTT_ROPE_MAX_AXES */
   int32_t pairs[TTT_ROPE_MAX_AXES]; /* pairs of each axis, each >= 1, at most TTT_ROPE_MAX_PAIRS in all */
   double base[TTT_ROPE_MAX_AXES];   /* each finite and > 0 */
@@ -90,8 +95,12 @@ int ttt_rope_apply(const ttt_rope* handle, int32_t B, int32_t H, int64_t N, cons
  *   dx = lam | (1 - a) lam;  da = lam h_{t-1} | lam (h_{t-1} - x);  dg = da a'(g);  dh0 = a_1 lam_1
  * States and products are fp32; g, x, h, dh, dg, dx are in `dtype`.  Products of the
  * gates of up to 256 tokens in a row are formed: gates that grow a state (|a| > 1) have to
- * keep them, and the states, within fp32's range; beyond it results are infinite or NaN,
- * in their channel and batch entry alone. */
+ * keep them, and the states, within fp32's range; beyond it, and from an infinite state
+ * on, results are infinite or NaN, in their channel and batch entry alone.
+ * TTT_ERR_UNSUPPORTED: L above 2^30; with c channels a column (bf16: 64, fp32: 32),
+ * B ceil(D / c) ceil(L / 256) above 2^30 forward, B ceil(D / c) ceil(L / 128) backward
+ * (sequences of up to 16 tokens are not cut so: for them, B ceil(D / 2) in bf16 or B D in
+ * fp32 above 2^38). */
 typedef enum { TTT_GATE_VALUE = 0, TTT_GATE_SIGMOID = 1, TTT_GATE_EXP = 2 } ttt_gate_kind;
 typedef enum { TTT_SCAN_PLAIN = 0, TTT_SCAN_COMPLEMENT = 1 } ttt_scan_input;
 
@@ -145,6 +154,10 @@ int ttt_scan_clear(const ttt_scan* handle, int32_t B, int64_t L, const int32_t* 
  *   dweight = sum dz xhat, dbias = sum dz (over tokens and batch entries); with q = dz weight
  *   dx = (q - mean(q) - xhat mean(q xhat)) / sqrt(var + eps)
  * Statistics, weight, bias and their gradients are fp32; x, y, dx, dy are in `dtype`.
+ * The statistics are those of all N tokens of the call: each output depends on later tokens
+ * as on earlier ones, and tokens that are handed over in parts, or one at a time, have
+ * other statistics than the whole.  It fits layers that see a whole image, view or clip, not
+ * causal or streamed ones (the layer's causal form, a state carried by the recurrence).
  * The strides' `head` is the distance between groups: C / groups for channels last
  * [B, N, C]; the layer's O [B, H, N, d] is read with groups = H. */
 typedef enum { TTT_ACT_NONE = 0, TTT_ACT_SILU = 1, TTT_ACT_GELU = 2 } ttt_act_kind;

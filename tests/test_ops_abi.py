@@ -261,3 +261,31 @@ def test_scan_keeps_the_states_that_backward_reads(L, states):
     st, h = _open("scan", ops.ScanConfig(D=33, gate=1, input=1, dtype=1))
     assert st == 0 and binding.LIB.ttt_scan_saved_size(h, 5, L) == 5 * states * 33 * 4
     binding.LIB.ttt_scan_destroy(h)
+
+
+def test_sizes_past_the_stated_limits_are_unsupported():
+    binding, ops = _lib()
+    for d, want in ((4096, 0), (4097, binding.TTT_ERR_UNSUPPORTED)):
+        st, h = _open("rope", _rope_cfg(d=d))
+        assert st == want, d
+        binding.LIB.ttt_rope_destroy(h)
+    st, h = _open("rope", _rope_cfg())
+    s = _s(1 << 47, 1 << 47, 64)
+    assert binding.LIB.ttt_rope_apply(h, 1, 1, (1 << 40) + 1, 1 << 50, s, 1 << 52, 0, 0, 1 << 54, s, 0,
+                                      None) == binding.TTT_ERR_UNSUPPORTED
+    binding.LIB.ttt_rope_destroy(h)
+    far = lambda k: k << 50  # noqa: E731
+    for dtype, c in ((0, 32), (1, 64)):
+        st, h = _open("scan", ops.ScanConfig(D=c + 1, gate=1, input=1, dtype=dtype))  # two columns of channels
+        assert st == 0
+        for backward, tile in ((False, 256), (True, 128)):
+            B, L = (1 << 28) + 1, tile + 1  # two tiles
+            s = _s(L * (c + 1), 0, c + 1)
+            if backward:
+                st = binding.LIB.ttt_scan_backward(h, B, L, far(1), s, None, far(2), s, far(3), s, None, far(4), far(5), s,
+                                                   far(6), s, None, far(7), 1 << 62, None, None)
+            else:
+                st = binding.LIB.ttt_scan_forward(h, B, L, far(1), s, far(2), s, None, None, far(3), s, None, None, far(7),
+                                                  1 << 62, None, None)
+            assert st == binding.TTT_ERR_UNSUPPORTED, (dtype, backward)
+        binding.LIB.ttt_scan_destroy(h)

@@ -213,9 +213,10 @@ int launch(RopeArgs& a, const RopeTable& tab, bool copy, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
 }
 
-// Heads of a thread: those that share its angles, the most that leave no more than one of
-// all heads' places empty (48672 tokens x 6 heads x 64 in halves: 14.1 us with six heads a
-// thread, 15.7 with three, 16.0 with two).  Narrow vectors have one form.
+// Heads of a thread: those that share its angles.  Six where six divides the heads (in halves,
+// whose pair takes two vectors), four where that leaves one place empty at most, else two (48672
+// tokens x 6 heads x 64 in halves: 14.1 us with six heads a thread, 15.7 with three, 16.0 with
+// two).  Narrow vectors have one form.
 template <class T, int BYTES, bool ONE>
 int launch_heads(RopeArgs& a, const RopeTable& tab, bool copy, cudaStream_t st) {
   if constexpr (BYTES < 16) {

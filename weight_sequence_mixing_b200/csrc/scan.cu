@@ -34,11 +34,11 @@
 // gates' gradient needs are formed again in fp32 from states that the forward pass kept
 // (one in 128 tokens, a backward tile), not read back rounded.
 //
-// Measured, bf16, 1024 channels: forward over 1029120 tokens 1.26 ms (77% of the copy
-// bandwidth; exponential gate), over 64 sequences of 2048 140 us (88%; plain gate), 181 us
+// Measured, bf16, 1024 channels: forward over 1029120 tokens 1.22 to 1.30 ms, box by box (79 to
+// 74% of the copy bandwidth; exponential gate), over 64 sequences of 2048 142 us (87%; plain gate), 187 us
 // with a sigmoid and its complement, where the exponentials and reciprocals keep their unit
-// 69% busy; backward 262 and 300 us (78 and 68%), bound by issue.  A single long chain adds
-// its latency: 131072 tokens take 167 us forward and 313 back.  Tiles half as long, two
+// 69% busy; backward 273 and 317 us (75 and 65%), bound by issue.  A single long chain adds
+// its latency: 131072 tokens take 168 us forward and 338 back.  Tiles half as long, two
 // blocks an SM, took 1.74 ms for the million tokens; one chain warp 2.30 (at that length).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

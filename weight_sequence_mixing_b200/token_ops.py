@@ -105,7 +105,7 @@ class _Op:
 
 
 class _StatusOp(_Op):
-    """An operator whose kernels wait on one another and report a wait that ran out."""
+    """An operator with a device status word, where a kernel that waits on other blocks reports a wait that ran out."""
 
     def check_status(self):
         """Waits for the device's work and raises if a call since the last check went wrong on the
@@ -189,6 +189,8 @@ class GroupNorm(_StatusOp):
 
     cfg: C, groups, act ("none", "silu", "gelu"; default "none"), eps (default 1e-5), dtype ("bf16", "f32").
     x is [B, N, C], or [B, groups, N, C / groups] as TTTLayer returns it; y is [B, N, C].
+    The statistics run over all N tokens of a call, later ones too: not for causal layers, nor for tokens that
+    come one at a time.  Its kernels wait on no other block, so check_status finds nothing of theirs.
     """
 
     def __post_init__(self):
