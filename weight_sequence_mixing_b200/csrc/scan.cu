@@ -37,7 +37,7 @@
 // Measured, bf16, 1024 channels: forward over 1029120 tokens 1.22 to 1.30 ms, box by box (79 to
 // 74% of the copy bandwidth; exponential gate), over 64 sequences of 2048 142 us (87%; plain gate), 187 us
 // with a sigmoid and its complement, where the exponentials and reciprocals keep their unit
-// 69% busy; backward 273 and 317 us (75 and 65%), bound by issue.  A single long chain adds
+// 68% busy; backward 273 and 317 us (75 and 65%), bound by issue.  A single long chain adds
 // its latency: 131072 tokens take 168 us forward and 338 back.  Tiles half as long, two
 // blocks an SM, took 1.74 ms for the million tokens; one chain warp 2.30 (at that length).
 #include <cuda_bf16.h>
